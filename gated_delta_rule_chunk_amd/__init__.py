@@ -14,6 +14,15 @@ not built, calls raise ``RuntimeError``.
                                                  d_final_state=None, cu_seqlens=None, scale=1.0)
     o = recurrent_step(q, k, v, g, beta, state_cache, state_slots=None, scale=1.0)
     device_check()      # raises KDAError if a kernel's bounded wait gave up since the last check
+
+The softmax attention over a latent that stands between the KDA layers
+(include/kda_mla.h): expanded for prompts and training, absorbed over a paged
+cache for generated tokens.
+
+    o, lse = mla_fwd(q, kv, k_rope, cu_seqlens_q=None, cu_seqlens_k=None, causal=True)
+    dq, dkv, dk_rope = mla_bwd(q, kv, k_rope, o, lse, d_o, ...)
+    mla_cache_append(latent, k_rope, cache, page_table, cache_lens)
+    o, lse = mla_step(q_latent, q_rope, cache, page_table, seq_lens, scale)
 """
 from __future__ import annotations
 
@@ -109,6 +118,19 @@ def load_library(path: str = LIB_PATH):
     lib.kda_chunk_bwd.argtypes = [P, P, P, P, P, P, P, P, P, I32, I32, I32, I32, I32, I32, F, ctypes.c_int,
                                   P, ctypes.c_size_t, P, P, P, P, P, P, P]
     lib.kda_chunk_bwd.restype = ctypes.c_int
+    I64, Z, D = ctypes.c_int64, ctypes.c_size_t, ctypes.c_int
+    lib.kda_mla_fwd.argtypes = [P, P, P, I64, I64, P, P] + [I32] * 8 + [F, D, I32, P, P, P]
+    lib.kda_mla_fwd.restype = ctypes.c_int
+    lib.kda_mla_bwd_workspace_bytes.argtypes = [I32] * 5
+    lib.kda_mla_bwd_workspace_bytes.restype = Z
+    lib.kda_mla_bwd.argtypes = [P, P, P, I64, I64, P, P, P, P, P] + [I32] * 8 + [F, D, I32, P, Z, P, P, P, P]
+    lib.kda_mla_bwd.restype = ctypes.c_int
+    lib.kda_mla_cache_append.argtypes = [P, I64, I64, P, I64, I64, P, P, P, P] + [I32] * 8 + [D, P]
+    lib.kda_mla_cache_append.restype = ctypes.c_int
+    lib.kda_mla_step_workspace_bytes.argtypes = [I32] * 6 + [D]
+    lib.kda_mla_step_workspace_bytes.restype = Z
+    lib.kda_mla_step.argtypes = [P, I64, I64, I64, P, I64, I64, I64, P, P, P] + [I32] * 8 + [F, D, P, Z, P, P, P]
+    lib.kda_mla_step.restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_last_error_message.argtypes = []
@@ -801,10 +823,232 @@ def recurrent_step_conv(xq, xk, xv, wq, wk, wv, conv_caches, g_logit, beta_logit
     return out
 
 
+def _need_rows(t, name, shape, dtype, device):
+    """Like _need for a tensor whose channels are contiguous and whose other
+    dimensions are strided (the library checks the strides' alignment)."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
+    if t.device != device:
+        raise ValueError(f"{name} is on {t.device}, expected {device}")
+    if t.numel() and t.stride(-1) != 1:
+        raise ValueError(f"{name} must be contiguous along its last dimension")
+
+
+def _workspace(workspace, need, dev):
+    if workspace is None:
+        return torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
+    if workspace.dtype != torch.uint8 or workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous uint8 tensor on the inputs' device")
+    return workspace
+
+
+def _steps(t, *dims):
+    """Strides of dimensions (0 along those of one element, where any value serves)."""
+    return [0 if t is None or t.shape[d] == 1 else t.stride(d) for d in dims]
+
+
+def _mla_inputs(q, kv, k_rope, cu_seqlens_q, cu_seqlens_k, scale):
+    if q.dim() != 4 or kv.dim() != 4:
+        raise ValueError("q must be [B,Tq,H,Dn+Dr] and kv [B,Tk,H,2*Dn]")
+    B, Tq, H, Dq = q.shape
+    Tk, dev, dt = kv.shape[1], q.device, q.dtype
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a GPU")
+    if dt not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    Dr = 0 if k_rope is None else k_rope.shape[-1]
+    Dn = Dq - Dr
+    _need(q, "q", (B, Tq, H, Dq), dt, dev)
+    _need(kv, "kv", (B, Tk, H, 2 * Dn), dt, dev)
+    if k_rope is not None:
+        _need_rows(k_rope, "k_rope", (B, Tk, Dr), dt, dev)
+    N = B
+    if (cu_seqlens_q is None) != (cu_seqlens_k is None):
+        raise ValueError("cu_seqlens_q and cu_seqlens_k come together")
+    if cu_seqlens_q is not None:
+        if cu_seqlens_q.dim() != 1:
+            raise ValueError("cu_seqlens_q must be 1-D")
+        N = cu_seqlens_q.numel() - 1
+        _need(cu_seqlens_q, "cu_seqlens_q", (N + 1,), torch.int32, dev)
+        _need(cu_seqlens_k, "cu_seqlens_k", (N + 1,), torch.int32, dev)
+    scale = float(Dq) ** -0.5 if scale is None else float(scale)
+    return B, Tq, Tk, H, Dn, Dr, N, dt, dev, scale
+
+
+def mla_fwd(q, kv, k_rope=None, cu_seqlens_q=None, cu_seqlens_k=None, causal=True, scale=None, out=None, lse=None):
+    """Latent attention, expanded form (kda_mla_fwd).
+
+    q [B,Tq,H,Dn+Dr], kv [B,Tk,H,2*Dn] (each head's key, then its value), both
+    contiguous; k_rope [B,Tk,Dr] or None (Dr = 0), rows may be strided; all
+    float32 or all bfloat16. cu_seqlens_q, cu_seqlens_k: int32 [N+1] (B must be
+    1) or None. scale: 1 / sqrt(Dn + Dr) if None. Returns (o [B,Tq,H,Dn], lse
+    [B,H,Tq] float32). Rows behind the last packed sequence are zeros (lse:
+    -inf) where ``out`` (``lse``) is not given, and left as they were otherwise.
+    """
+    lib = load_library()
+    B, Tq, Tk, H, Dn, Dr, N, dt, dev, scale = _mla_inputs(q, kv, k_rope, cu_seqlens_q, cu_seqlens_k, scale)
+    if (out is None) != (lse is None):
+        raise ValueError("out and lse come together")
+    rest = out is None
+    if rest:
+        out = torch.empty((B, Tq, H, Dn), dtype=dt, device=dev)
+        lse = torch.empty((B, H, Tq), dtype=torch.float32, device=dev)
+    else:
+        _need(out, "out", (B, Tq, H, Dn), dt, dev)
+        _need(lse, "lse", (B, H, Tq), torch.float32, dev)
+    row, batch = _steps(k_rope, 1, 0)
+    with torch.cuda.device(dev):
+        _check(lib.kda_mla_fwd(_ptr(q), _ptr(kv), _ptr(k_rope), row, batch, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B,
+                               Tq, Tk, H, Dn, Dr, N, int(bool(causal)), scale, _DTYPES[dt], int(rest), _ptr(out),
+                               _ptr(lse), _stream(dev)))
+    return out, lse
+
+
+def mla_bwd_workspace_bytes(B, Tq, Tk, H, Dr):
+    """Bytes of workspace kda_mla_bwd needs."""
+    return int(load_library().kda_mla_bwd_workspace_bytes(B, Tq, Tk, H, Dr))
+
+
+def mla_bwd(q, kv, k_rope, o, lse, d_o, cu_seqlens_q=None, cu_seqlens_k=None, causal=True, scale=None, dq=None,
+            dkv=None, dk_rope=None, workspace=None):
+    """Gradients of ``mla_fwd`` (kda_mla_bwd): o and lse are what it returned
+    for the same arguments, d_o [B,Tq,H,Dn] the incoming gradient. Returns (dq,
+    dkv, dk_rope or None) in the inputs' dtype. Rows behind the last packed
+    sequence are zeros if no output is given, and left as they were otherwise.
+    """
+    lib = load_library()
+    B, Tq, Tk, H, Dn, Dr, N, dt, dev, scale = _mla_inputs(q, kv, k_rope, cu_seqlens_q, cu_seqlens_k, scale)
+    _need(o, "o", (B, Tq, H, Dn), dt, dev)
+    _need(lse, "lse", (B, H, Tq), torch.float32, dev)
+    _need(d_o, "d_o", (B, Tq, H, Dn), dt, dev)
+    given = [x is not None for x in ((dq, dkv) if k_rope is None else (dq, dkv, dk_rope))]
+    if any(given) and not all(given):
+        raise ValueError("dq, dkv and dk_rope come together")
+    rest = not any(given)
+    if rest:
+        dq, dkv = torch.empty_like(q), torch.empty_like(kv)
+        dk_rope = None if k_rope is None else torch.empty((B, Tk, Dr), dtype=dt, device=dev)
+    else:
+        _need(dq, "dq", q.shape, dt, dev)
+        _need(dkv, "dkv", kv.shape, dt, dev)
+        if k_rope is not None:
+            _need(dk_rope, "dk_rope", (B, Tk, Dr), dt, dev)
+    workspace = _workspace(workspace, mla_bwd_workspace_bytes(B, Tq, Tk, H, Dr), dev)
+    row, batch = _steps(k_rope, 1, 0)
+    with torch.cuda.device(dev):
+        _check(lib.kda_mla_bwd(_ptr(q), _ptr(kv), _ptr(k_rope), row, batch, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
+                               _ptr(o), _ptr(lse), _ptr(d_o), B, Tq, Tk, H, Dn, Dr, N, int(bool(causal)), scale,
+                               _DTYPES[dt], int(rest), _ptr(workspace), workspace.numel(), _ptr(dq), _ptr(dkv),
+                               _ptr(dk_rope), _stream(dev)))
+    return dq, dkv, dk_rope
+
+
+def _mla_cache(cache, page_table, lens, name, dt, dev, N):
+    if cache.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("cache must be [n_pages,page_size,Dc+Dr] and page_table [N,max_pages]")
+    n_pages, page_size, D = cache.shape
+    _need(cache, "cache", (n_pages, page_size, D), dt, dev)
+    _need(page_table, "page_table", (N, page_table.shape[1]), torch.int32, dev)
+    _need(lens, name, (N,), torch.int32, dev)
+    return n_pages, page_size, page_table.shape[1], D
+
+
+def mla_cache_append(latent, k_rope, cache, page_table, cache_lens, cu_seqlens=None):
+    """Write new tokens into the paged cache of latents (kda_mla_cache_append).
+
+    latent [B,T,Dc], k_rope [B,T,Dr] or None (rows may be strided); cache
+    [n_pages,page_size,Dc+Dr]; page_table int32 [N,max_pages]; cache_lens int32
+    [N], the lengths before the call (negative: padding row), not changed;
+    cu_seqlens int32 [N+1] (B must be 1) or None (N = B). Pages that do not
+    exist are reported by ``device_check``."""
+    lib = load_library()
+    if latent.dim() != 3:
+        raise ValueError("latent must be [B,T,Dc]")
+    B, T, Dc = latent.shape
+    dev, dt = latent.device, latent.dtype
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a GPU")
+    if dt not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    Dr = 0 if k_rope is None else k_rope.shape[-1]
+    _need_rows(latent, "latent", (B, T, Dc), dt, dev)
+    if k_rope is not None:
+        _need_rows(k_rope, "k_rope", (B, T, Dr), dt, dev)
+    N = B
+    if cu_seqlens is not None:
+        if cu_seqlens.dim() != 1:
+            raise ValueError("cu_seqlens must be 1-D")
+        N = cu_seqlens.numel() - 1
+        _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
+    n_pages, page_size, max_pages, D = _mla_cache(cache, page_table, cache_lens, "cache_lens", dt, dev, N)
+    if D != Dc + Dr:
+        raise ValueError(f"cache rows have {D} channels, latent and k_rope {Dc + Dr}")
+    lrow, lbatch = _steps(latent, 1, 0)
+    krow, kbatch = _steps(k_rope, 1, 0)
+    with torch.cuda.device(dev):
+        _check(lib.kda_mla_cache_append(_ptr(latent), lrow, lbatch, _ptr(k_rope), krow, kbatch, _ptr(cache),
+                                        _ptr(page_table), _ptr(cache_lens), _ptr(cu_seqlens), n_pages, page_size,
+                                        max_pages, B, T, Dc, Dr, N, _DTYPES[dt], _stream(dev)))
+
+
+def mla_step_workspace_bytes(Nb, Tq, H, Dc, page_size, max_pages, dtype):
+    """Bytes of workspace kda_mla_step needs."""
+    return int(load_library().kda_mla_step_workspace_bytes(Nb, Tq, H, Dc, page_size, max_pages, _DTYPES[dtype]))
+
+
+def mla_step(q_latent, q_rope, cache, page_table, seq_lens, scale, out=None, lse=None, workspace=None):
+    """Latent attention of Tq new tokens per row over the paged cache, absorbed
+    form (kda_mla_step).
+
+    q_latent [Nb,Tq,H,Dc], q_rope [Nb,Tq,H,Dr] or None, any strides with
+    contiguous channels; cache [n_pages,page_size,Dc+Dr], which holds the new
+    tokens already; page_table int32 [Nb,max_pages]; seq_lens int32 [Nb] with
+    the new tokens counted (<= 0: padding row). scale: of the expanded head, 1 /
+    sqrt(Dn + Dr). Returns (o [Nb,Tq,H,Dc] in latent space, lse [Nb,Tq,H]
+    float32). Pages that do not exist are reported by ``device_check``."""
+    lib = load_library()
+    if q_latent.dim() != 4:
+        raise ValueError("q_latent must be [Nb,Tq,H,Dc]")
+    Nb, Tq, H, Dc = q_latent.shape
+    dev, dt = q_latent.device, q_latent.dtype
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a GPU")
+    if dt not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dt}")
+    Dr = 0 if q_rope is None else q_rope.shape[-1]
+    _need_rows(q_latent, "q_latent", (Nb, Tq, H, Dc), dt, dev)
+    if q_rope is not None:
+        _need_rows(q_rope, "q_rope", (Nb, Tq, H, Dr), dt, dev)
+    n_pages, page_size, max_pages, D = _mla_cache(cache, page_table, seq_lens, "seq_lens", dt, dev, Nb)
+    if D != Dc + Dr:
+        raise ValueError(f"cache rows have {D} channels, q_latent and q_rope {Dc + Dr}")
+    if out is None:
+        out = torch.empty((Nb, Tq, H, Dc), dtype=dt, device=dev)
+    else:
+        _need(out, "out", (Nb, Tq, H, Dc), dt, dev)
+    if lse is None:
+        lse = torch.empty((Nb, Tq, H), dtype=torch.float32, device=dev)
+    else:
+        _need(lse, "lse", (Nb, Tq, H), torch.float32, dev)
+    workspace = _workspace(workspace, mla_step_workspace_bytes(Nb, Tq, H, Dc, page_size, max_pages, dt), dev)
+    with torch.cuda.device(dev):
+        _check(lib.kda_mla_step(_ptr(q_latent), *_steps(q_latent, 0, 1, 2), _ptr(q_rope), *_steps(q_rope, 0, 1, 2),
+                                _ptr(cache), _ptr(page_table), _ptr(seq_lens), n_pages, page_size, max_pages, Nb, Tq,
+                                H, Dc, Dr, float(scale), _DTYPES[dt], _ptr(workspace), workspace.numel(), _ptr(out),
+                                _ptr(lse), _stream(dev)))
+    return out, lse
+
+
 def device_check(device=None):
     """Wait for torch's current stream on ``device`` and raise ``KDAError``
-    (status KDA_ERR_DEVICE) if a bounded wait of any library kernel on that
-    device gave up since the previous check."""
+    (status KDA_ERR_DEVICE) if, since the previous check, a bounded wait of any
+    library kernel on that device gave up, or a call met inputs that only the
+    device can see to be wrong (log-decays out of range, cache pages that do
+    not exist)."""
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     lib = load_library()
     with torch.cuda.device(dev):

@@ -7,7 +7,8 @@ Each pairs one of the library's forward calls with its backward call:
 the ISEEKYAN/k3 README names for the KDA layer (its compute-path paragraph);
 the arguments are this library's. With ``segments`` > 1 the forward runs the
 intra-sequence split (kda_chunk_fwd_split, _split_prologue), which computes the
-same function, so its gradient is the same backward call's. Every step runs in
+same function, so its gradient is the same backward call's. ``mla`` pairs the
+expanded latent attention's calls (kda_mla_fwd / kda_mla_bwd). Every step runs in
 the library's kernels: this module saves the inputs, routes the incoming
 gradients to the backward call and casts the float32 gradients to each input's
 dtype.
@@ -15,7 +16,7 @@ dtype.
 import torch
 
 from . import (chunk_bwd, chunk_bwd_conv, chunk_bwd_prologue, chunk_fwd, chunk_fwd_conv, chunk_fwd_prologue,
-               chunk_fwd_split, chunk_fwd_split_prologue)
+               chunk_fwd_split, chunk_fwd_split_prologue, mla_bwd, mla_fwd)
 
 
 def _contig(t):
@@ -129,3 +130,26 @@ def chunk_kda_conv(xq, xk, xv, wq, wk, wv, g_logit, beta_logit, A_log, dt_bias, 
                                           cs[0], cs[1], cs[2], cu_seqlens, float(scale), float(gate_lower_bound),
                                           float(l2_eps), bool(activation), int(chunk_size))
     return o, fin, (cq, ck, cv)
+
+
+class _Mla(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, q, kv, k_rope, cu_q, cu_k, causal, scale):
+        o, lse = mla_fwd(q, kv, k_rope, cu_seqlens_q=cu_q, cu_seqlens_k=cu_k, causal=causal, scale=scale)
+        ctx.save_for_backward(q, kv, k_rope, cu_q, cu_k, o, lse)
+        ctx.args = (causal, scale)
+        return o
+
+    @staticmethod
+    def backward(ctx, d_o):
+        q, kv, k_rope, cu_q, cu_k, o, lse = ctx.saved_tensors
+        causal, scale = ctx.args
+        dq, dkv, dkr = mla_bwd(q, kv, k_rope, o, lse, _contig(d_o), cu_seqlens_q=cu_q, cu_seqlens_k=cu_k,
+                               causal=causal, scale=scale)
+        return dq, dkv, dkr, None, None, None, None
+
+
+def mla(q, kv, k_rope=None, cu_seqlens_q=None, cu_seqlens_k=None, causal=True, scale=None):
+    """Differentiable ``mla_fwd``: returns o. Gradients reach q, kv and k_rope
+    (kda_mla_bwd). lse is not returned: it has no gradient here."""
+    return _Mla.apply(q, kv, k_rope, cu_seqlens_q, cu_seqlens_k, bool(causal), None if scale is None else float(scale))

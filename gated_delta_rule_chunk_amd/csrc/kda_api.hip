@@ -14,8 +14,10 @@
 // Device status words, counted since the module was loaded on this device:
 // [0] bounded waits between waves (in any kernel of this library) that gave
 // up; [1] waves of the matrix-core forward or backward that met log-decays out
-// of the range they need. Kernels add to them with a vector atomic from one lane; the host
-// only reads them (kda_device_check). The rest of the array is padding.
+// of the range they need; [2] cache pages that a latent-attention call was
+// pointed to and that do not exist. Kernels add to them with a vector atomic
+// from one lane; the host only reads them (kda_device_check). The rest of the
+// array is padding.
 __device__ __attribute__((aligned(256))) unsigned int kda_device_status[64];
 
 namespace {
@@ -23,7 +25,7 @@ namespace {
 constexpr int kMaxDevices = 64;
 std::mutex g_dev_mutex;
 unsigned int* g_status_ptr[kMaxDevices] = {};
-unsigned int g_status_seen[kMaxDevices][2] = {};   // [0] wait give-ups, [1] gates out of range
+unsigned int g_status_seen[kMaxDevices][3] = {};   // [0] wait give-ups, [1] gates out of range, [2] pages
 std::atomic<int> g_spin_limit{1 << 22};
 
 }  // namespace
@@ -51,6 +53,17 @@ int wait_spin_limit() { return g_spin_limit.load(std::memory_order_relaxed); }
 namespace {
 
 thread_local char g_last_error[512] = "";
+
+}  // namespace
+
+namespace kda {
+
+void set_error(const char* fmt, va_list ap) { vsnprintf(g_last_error, sizeof(g_last_error), fmt, ap); }
+void clear_error() { g_last_error[0] = 0; }
+
+}  // namespace kda
+
+namespace {
 
 kda_status fail(kda_status st, const char* fmt, ...) {
     va_list ap;
@@ -95,17 +108,17 @@ kda_status kda_device_check(void* stream) {
     int dev = 0;
     if (!word || hipGetDevice(&dev) != hipSuccess)
         return fail(KDA_ERR_HIP, "kda_device_check: the device status word is not accessible");
-    unsigned int now[2] = {0, 0};
+    unsigned int now[3] = {0, 0, 0};
     hipError_t e = hipMemcpyAsync(now, word, sizeof(now), hipMemcpyDeviceToHost, s);
     if (e == hipSuccess) e = hipStreamSynchronize(s);
     if (e != hipSuccess) return fail(KDA_ERR_HIP, "kda_device_check: %s", hipGetErrorString(e));
-    unsigned int seen[2];
+    unsigned int seen[3];
     {
         std::lock_guard<std::mutex> lock(g_dev_mutex);
-        seen[0] = g_status_seen[dev][0];
-        seen[1] = g_status_seen[dev][1];
-        g_status_seen[dev][0] = now[0];
-        g_status_seen[dev][1] = now[1];
+        for (int i = 0; i < 3; ++i) {
+            seen[i] = g_status_seen[dev][i];
+            g_status_seen[dev][i] = now[i];
+        }
     }
     if (now[0] != seen[0])
         return fail(KDA_ERR_DEVICE,
@@ -118,6 +131,11 @@ kda_status kda_device_check(void* stream) {
                     "chunk's total outside [-84, 0]; backward: a g outside [-5, 0]; NaN included) in %u wave(s) on "
                     "device %d since the last check; the outputs of the calls that ran meanwhile are not valid",
                     now[1] - seen[1], dev);
+    if (now[2] != seen[2])
+        return fail(KDA_ERR_DEVICE,
+                    "kda_device_check: latent-attention calls met rows of a sequence past its page table or in pages "
+                    "outside [0, n_pages) (%u counted) on device %d since the last check; those rows were skipped",
+                    now[2] - seen[2], dev);
     return KDA_OK;
 }
 

@@ -3,6 +3,7 @@
 #pragma once
 
 #include <hip/hip_runtime.h>
+#include <stdarg.h>
 #include <stdint.h>
 
 namespace kda {
@@ -59,6 +60,9 @@ struct ChunkArgs {
 // bounded wait (both owned by the C ABI).
 unsigned int* device_status_word();
 int wait_spin_limit();
+// The calling thread's error message (owned by the C ABI).
+void set_error(const char* fmt, va_list ap);
+void clear_error();
 
 struct StepArgs {
     const void* q;
@@ -228,5 +232,68 @@ hipError_t launch_chunk_generic(const ChunkArgs& a, hipStream_t s);  // any supp
 hipError_t launch_recurrent_step(const StepArgs& a, hipStream_t s);
 
 bool chunk_mfma_supported(const ChunkArgs& a);
+
+// Latent attention, expanded form (kda_mla_fwd, kda_mla_bwd).
+struct MlaArgs {
+    const void* q;              // [B,Tq,H,Dn+Dr]
+    const void* kv;             // [B,Tk,H,2*Dn]: keys, then values
+    const void* kr;             // [B,Tk,Dr], rows kr_row elements apart, batches kr_batch; nullptr when Dr = 0
+    int64_t kr_row, kr_batch;
+    const int32_t* cuq;         // [N+1] or nullptr
+    const int32_t* cuk;
+    void* o;                    // [B,Tq,H,Dn] (backward: input)
+    float* lse;                 // [B,H,Tq] (backward: input) or nullptr
+    int32_t B, Tq, Tk, H, Dn, Dr, N;
+    bool causal, bf16;
+    bool zero_rest;             // write zeros (lse: -inf) to the rows behind the last packed sequence
+    float scale;
+    // backward
+    const void* d_o;            // [B,Tq,H,Dn]
+    void* dq;
+    void* dkv;
+    void* dkr;                  // [B,Tk,Dr] contiguous, nullptr when Dr = 0
+    float* delta;               // workspace [B,H,Tq]: sum of d_o * o over a row
+    float* dkr_part;            // workspace [H,B,Tk,Dr]: per-head gradients of the shared key part
+};
+
+// Absorbed form over a paged cache of latents (kda_mla_step), and its write
+// (kda_mla_cache_append).
+struct MlaStepArgs {
+    const void* ql;             // [Nb,Tq,H,Dc], strides in elements
+    int64_t ql_b, ql_t, ql_h;
+    const void* qr;             // [Nb,Tq,H,Dr] or nullptr when Dr = 0
+    int64_t qr_b, qr_t, qr_h;
+    const void* cache;          // [n_pages,page_size,Dc+Dr]
+    const int32_t* table;       // [Nb,max_pages]
+    const int32_t* lens;        // [Nb]
+    void* o;                    // [Nb,Tq,H,Dc]
+    float* lse;                 // [Nb,Tq,H] or nullptr
+    float* part;                // workspace
+    unsigned int* status;       // counts keys in pages that do not exist
+    int32_t n_pages, page_shift, max_pages, Nb, Tq, H, Dc, Dr;
+    int32_t blocks, groups, parts, min_tiles;  // the split (mla_step_plan)
+    float scale;
+    bool bf16;
+};
+struct MlaAppendArgs {
+    const void* latent;         // [B,T,Dc], strides in elements
+    int64_t lat_row, lat_batch;
+    const void* kr;             // [B,T,Dr] or nullptr when Dr = 0
+    int64_t kr_row, kr_batch;
+    void* cache;
+    const int32_t* table;       // [N,max_pages]
+    const int32_t* lens;        // [N] lengths before the call
+    const int32_t* cu;          // [N+1] or nullptr
+    unsigned int* status;
+    int32_t n_pages, page_shift, max_pages, B, T, Dc, Dr, N;
+    bool bf16;
+};
+
+// Fills the split of a decode call and returns its workspace in bytes.
+size_t mla_step_plan(MlaStepArgs& a);
+hipError_t launch_mla_step(const MlaStepArgs& a, hipStream_t stream);
+hipError_t launch_mla_append(const MlaAppendArgs& a, hipStream_t stream);
+hipError_t launch_mla_fwd(const MlaArgs& a, hipStream_t stream);
+hipError_t launch_mla_bwd(const MlaArgs& a, hipStream_t stream);
 
 }  // namespace kda

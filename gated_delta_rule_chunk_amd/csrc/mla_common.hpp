@@ -1,0 +1,300 @@
+// Device helpers shared by the latent-attention kernels (gfx950 only).
+//
+// All matrix products run on 32x32 tiles with 16 products per element and
+// instruction group ("step"), for bf16 one v_mfma_f32_32x32x16_bf16, for
+// float32 eight v_mfma_f32_32x32x2f32 on the same logical operands. Operand
+// layout of a step, for lane l with n = l % 32, hf = l / 32: A row n and B
+// column n, products 8 hf .. 8 hf + 7. Accumulator register r of lane l is
+// row 8 (r / 4) + 4 hf + r % 4, column n.
+//
+// The scores are formed transposed (rows = keys, columns = queries), so a
+// lane's 16 accumulator registers all belong to one query: the softmax needs
+// one exchange with lane l ^ 32 and no shared memory. Registers 8 s .. 8 s + 7
+// are then, as they stand, the B operand of a step over 16 keys if the A
+// operand takes its products in the same order: product j of half hf is key
+// 4 hf + j for j < 4 and 8 + 4 hf + j - 4 for j >= 4 ("register order").
+#pragma once
+
+#include <type_traits>
+
+#include "device_common.hpp"
+
+namespace kda {
+namespace mla {
+
+typedef float f32x16 __attribute__((ext_vector_type(16)));
+typedef float f32x8 __attribute__((ext_vector_type(8)));
+typedef short s16x4 __attribute__((ext_vector_type(4)));
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+#define KDA_LDS __attribute__((address_space(3)))
+
+template <class T> struct Elem;
+template <> struct Elem<__bf16> {
+    using Frag = bf16x8;
+};
+template <> struct Elem<float> {
+    using Frag = f32x8;
+};
+template <class T> using Frag = typename Elem<T>::Frag;
+// elements of T in a 16-byte chunk
+template <class T> constexpr int kChunk = 16 / (int)sizeof(T);
+
+__device__ __forceinline__ f32x16 mma(bf16x8 a, bf16x8 b, f32x16 c) {
+    return __builtin_amdgcn_mfma_f32_32x32x16_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x16 mma(f32x8 a, f32x8 b, f32x16 c) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+}
+__device__ __forceinline__ f32x16 zero16() {
+    f32x16 z;
+#pragma unroll
+    for (int r = 0; r < 16; ++r) z[r] = 0.f;
+    return z;
+}
+
+// LDS tiles: rows of RC 16-byte chunks (RC a multiple of 8) with no padding,
+// chunk c of row r at position c ^ swizzle(r), so that the 16 rows of an
+// operand read, and the 4 chunks of 4 or 8 consecutive rows of a transposed
+// read, lie in different banks. Loads straight from global memory fill LDS in
+// the order of the lanes, so padding is not possible; the source address of
+// each lane carries the permutation instead.
+template <int RC> __device__ __forceinline__ int swizzle(int r) {
+    if constexpr (RC % 16 == 0) {
+        return ((r & 3) << 2) | ((r >> 2) & 3);
+    } else {   // 8 mod 16: odd rows are half a bank cycle away already
+        return (((r >> 1) & 1) << 2) | ((r >> 2) & 3);
+    }
+}
+
+// 16 bytes per lane from global memory to LDS at `lds` (uniform) + 16 * lane.
+// Written as an instruction so that the compiler, which cannot tell the two
+// buffers apart, does not wait for the next tile before it reads this one;
+// wait_loads() and the barrier order them. It has no register output.
+__device__ __forceinline__ void load_lds16(const char* g, char* lds) {
+    const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(KDA_LDS char*)lds);
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(base), "v"(g) : "memory");
+}
+
+// Rows [0, ROWS) of a tile from global rows g + r * stride bytes (r clamped
+// to rmax) to LDS, NT threads (wave w, uniform), not waited for. ROWS * RC is a multiple of NT.
+template <int RC, int ROWS, int NT>
+__device__ __forceinline__ void load_tile(char* lds, const char* g, int64_t stride, int rmax, int w, int lane) {
+    static_assert(ROWS * RC % NT == 0 && NT % 64 == 0, "whole instructions");
+#pragma unroll
+    for (int i = 0; i < ROWS * RC / NT; ++i) {
+        const int s = i * NT + w * 64 + lane;
+        const int r = s / RC, c = (s % RC) ^ swizzle<RC>(r);
+        const int rr = r < rmax ? r : rmax;
+        load_lds16(g + rr * stride + c * 16, lds + (i * NT + w * 64) * 16);
+    }
+}
+
+// Byte offset in a row of chunk k + x (k a multiple of 2 known when compiling,
+// x the lane's part, below 8 with k's bits clear) under swizzle sw. Written so
+// that few registers serve many k: chunks are permuted within groups of 16
+// (or 8), and the group goes into the instruction's offset.
+template <int RC> __device__ __forceinline__ int chunk_at(int k, int x, int sw) {
+    constexpr int G = RC % 16 == 0 ? 16 : 8;
+    return (((x ^ sw) ^ (k & (G - 1))) << 4) + (k / G * G) * 16;
+}
+
+// Operand of one step over the columns: row r, products = columns
+// 16 step + 8 hf .. + 7. (The x argument: 2 * half more for steps that two
+// waves take in turn, with step = 2 * (step of the wave).)
+template <class T, int RC>
+__device__ __forceinline__ Frag<T> read_rows(const char* lds, int r, int step, int hf, int odd = 0) {
+    const char* p = lds + r * (RC * 16);
+    const int sw = swizzle<RC>(r);
+    if constexpr (sizeof(T) == 2) {
+        return *reinterpret_cast<const bf16x8*>(p + chunk_at<RC>(2 * step, 2 * odd + hf, sw));
+    } else {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(p + chunk_at<RC>(4 * step, 4 * odd + 2 * hf, sw));
+        const f32x4 b = *reinterpret_cast<const f32x4*>(p + chunk_at<RC>(4 * step, 4 * odd + 2 * hf + 1, sw));
+        return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+}
+
+// Operand of one step over the rows: operand row n = column col0 + n of the
+// tile, products = rows row0 .. row0 + 15 in register order (above). bf16
+// uses the transposing LDS read: each 16 lanes read a 4 x 16 block, 8 bytes
+// per lane, and lane i of them receives column i.
+template <class T, int RC> __device__ __forceinline__ Frag<T> read_cols(const char* lds, int row0, int col0, int lane) {
+    if constexpr (sizeof(T) == 2) {
+        bf16x8 f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = 8 * u + 4 * (lane >> 5) + ((lane >> 2) & 3);      // row0 is a multiple of 16
+            const int x = 2 * ((lane >> 4) & 1) + ((lane & 3) >> 1);
+            const char* p = lds + r * (RC * 16) + (lane & 1) * 8 + row0 * (RC * 16) +
+                            chunk_at<RC>(col0 >> 3, x, swizzle<RC>(r));
+            const s16x4 v = __builtin_amdgcn_ds_read_tr16_b64_v4i16((KDA_LDS s16x4*)p);
+            const bf16x4 b = __builtin_bit_cast(bf16x4, v);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[4 * u + j] = b[j];
+        }
+        return f;
+    } else {
+        f32x8 f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = 8 * (j >> 2) + 4 * (lane >> 5) + (j & 3);
+            f[j] = *reinterpret_cast<const float*>(lds + r * (RC * 16) + (lane & 3) * 4 + row0 * (RC * 16) +
+                                                   chunk_at<RC>(col0 >> 2, (lane & 31) >> 2, swizzle<RC>(r)));
+        }
+        return f;
+    }
+}
+
+// Eight consecutive elements of a row in global memory.
+template <class T> __device__ __forceinline__ Frag<T> load8(const T* p) {
+    if constexpr (sizeof(T) == 2) {
+        return *reinterpret_cast<const bf16x8*>(p);
+    } else {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+        return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+}
+
+// Accumulator registers 8 s .. 8 s + 7 as an operand. bf16 rounds here, once,
+// to the nearest: the matrix cores take bf16, and the statistics stay float32.
+template <class T> __device__ __forceinline__ Frag<T> to_frag(const f32x16& x, int s) {
+    Frag<T> f;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = (T)x[8 * s + j];
+    return f;
+}
+
+// max / sum over a lane and its other half
+__device__ __forceinline__ float half_max(float v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1]));
+}
+__device__ __forceinline__ float half_sum(float v) {
+    const auto p = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return __uint_as_float(p[0]) + __uint_as_float(p[1]);
+}
+
+// Stores a 32 x 32 accumulator (transposed: lane column n = output row, rows
+// = 32 consecutive output columns) times mul to p = that row's first of the
+// 32 columns. The two halves of a lane pair exchange registers so that each
+// stores 8 consecutive columns. Every lane takes part in the exchange; only
+// lanes with `live` store.
+template <class T>
+__device__ __forceinline__ void store_tile(T* p, const f32x16& acc, float mul, int hf, bool live) {
+#pragma unroll
+    for (int g = 0; g < 4; g += 2) {
+        if constexpr (sizeof(T) == 2) {
+            const uint32_t a0 = pack2_bf16(acc[4 * g] * mul, acc[4 * g + 1] * mul);
+            const uint32_t a1 = pack2_bf16(acc[4 * g + 2] * mul, acc[4 * g + 3] * mul);
+            const uint32_t b0 = pack2_bf16(acc[4 * g + 4] * mul, acc[4 * g + 5] * mul);
+            const uint32_t b1 = pack2_bf16(acc[4 * g + 6] * mul, acc[4 * g + 7] * mul);
+            const auto x0 = __builtin_amdgcn_permlane32_swap(a0, b0, false, false);
+            const auto x1 = __builtin_amdgcn_permlane32_swap(a1, b1, false, false);
+            if (live) *reinterpret_cast<u32x4*>(p + 8 * (g + hf)) = u32x4{x0[0], x1[0], x0[1], x1[1]};
+        } else {
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const f32x4 v = {acc[4 * (g + k)] * mul, acc[4 * (g + k) + 1] * mul, acc[4 * (g + k) + 2] * mul,
+                                 acc[4 * (g + k) + 3] * mul};
+                if (live) *reinterpret_cast<f32x4*>(p + 8 * (g + k) + 4 * hf) = v;
+            }
+        }
+    }
+}
+
+// The workgroup barrier without a fence: every wave has waited for its own
+// loads into LDS and consumed its own reads before it.
+__device__ __forceinline__ void wg_barrier() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
+}
+__device__ __forceinline__ void wait_loads() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0); the builtin, so that the compiler knows of it
+    asm volatile("" ::: "memory");
+}
+
+// Blocks are dealt round-robin over the 8 XCDs, each with an L2 of its own:
+// this gives XCD x the x-th contiguous eighth of a list of n items, so that
+// the items that share data (a head's tiles) share an L2. Returns -1 past the
+// end. The grid is 8 * ceil(n / 8) blocks.
+__device__ __forceinline__ int64_t xcd_item(int64_t n) {
+    const int64_t per = (n + 7) / 8, i = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
+    return (int64_t)(blockIdx.x >> 3) < per && i < n ? i : -1;
+}
+
+// Start and length of sequence n (dense: rows of T; packed: offsets cu,
+// clipped to [0, T] so that no value in it leads outside the tensor). Packed
+// sequence N is the rows behind the last one.
+__device__ __forceinline__ void seq_range(const int32_t* cu, int N, int n, int T, int64_t& start, int& len) {
+    if (!cu) {
+        start = (int64_t)n * T;
+        len = T;
+        return;
+    }
+    int a = cu[n], b = n < N ? cu[n + 1] : T;
+    a = a < 0 ? 0 : a > T ? T : a;
+    b = b < a ? a : b > T ? T : b;
+    start = a;
+    len = b - a;
+}
+
+// Packed sequences (the rows behind the last one counted as a sequence more)
+// cut into tiles of `tile` rows: the sequence and tile of slot t in the list
+// of all tiles; false past its end, which is at most T / tile + N + 1. A wave
+// takes 64 sequences at a time (their tile counts summed over the lanes).
+__device__ __forceinline__ bool find_tile(const int32_t* cu, int N, int T, int tile, int64_t t, int lane, int& n, int& k) {
+    int64_t before = 0;
+    for (int n0 = 0; n0 <= N; n0 += 64) {
+        int cnt = 0;
+        if (n0 + lane <= N) {
+            int64_t s;
+            int len;
+            seq_range(cu, N, n0 + lane, T, s, len);
+            cnt = (len + tile - 1) / tile;
+        }
+        int sum = cnt;
+#pragma unroll
+        for (int d = 1; d < 64; d <<= 1) {
+            const int v = __shfl_up(sum, d);
+            sum += lane >= d ? v : 0;
+        }
+        const int total = __builtin_amdgcn_readlane(sum, 63);
+        if (t < before + total) {
+            const int l = __ffsll((unsigned long long)__ballot(before + sum > t)) - 1;
+            n = n0 + l;
+            k = (int)(t - before) - (__builtin_amdgcn_readlane(sum, l) - __builtin_amdgcn_readlane(cnt, l));
+            return true;
+        }
+        before += total;
+    }
+    return false;
+}
+
+// Tile `slot` of the list of all tiles of `tile` rows over B dense or N packed
+// sequences of [.., T, ..]: its sequence n, that sequence's start and length,
+// the tile's first row r0; false past the end of the list.
+__device__ __forceinline__ bool tile_of(const int32_t* cu, int N, int T, int tile, int64_t slot, int lane, int& n,
+                                        int64_t& start, int& len, int& r0) {
+    int k;
+    if (cu) {
+        if (!find_tile(cu, N, T, tile, slot, lane, n, k)) return false;
+    } else {
+        const int per = (T + tile - 1) / tile;
+        n = (int)(slot / per);
+        k = (int)(slot % per);
+    }
+    seq_range(cu, N, n, T, start, len);
+    r0 = k * tile;
+    return true;
+}
+// length of that list, at most
+inline int64_t tile_slots(const int32_t* cu, int B, int N, int T, int tile) {
+    return cu ? (int64_t)T / tile + N + 1 : (int64_t)B * ((T + tile - 1) / tile);
+}
+
+}  // namespace mla
+}  // namespace kda

@@ -26,6 +26,7 @@ cache for generated tokens.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 import os
 import re
@@ -838,6 +839,14 @@ def _need_rows(t, name, shape, dtype, device):
         raise ValueError(f"{name} must be contiguous along its last dimension")
 
 
+_HERE_ALREADY = contextlib.nullcontext()
+
+
+def _on(dev):
+    """Makes dev the current device for a launch, where it is not already."""
+    return _HERE_ALREADY if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+
+
 def _workspace(workspace, need, dev):
     if workspace is None:
         return torch.empty((max(need, 16),), dtype=torch.uint8, device=dev)
@@ -901,7 +910,7 @@ def mla_fwd(q, kv, k_rope=None, cu_seqlens_q=None, cu_seqlens_k=None, causal=Tru
         _need(out, "out", (B, Tq, H, Dn), dt, dev)
         _need(lse, "lse", (B, H, Tq), torch.float32, dev)
     row, batch = _steps(k_rope, 1, 0)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib.kda_mla_fwd(_ptr(q), _ptr(kv), _ptr(k_rope), row, batch, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k), B,
                                Tq, Tk, H, Dn, Dr, N, int(bool(causal)), scale, _DTYPES[dt], int(rest), _ptr(out),
                                _ptr(lse), _stream(dev)))
@@ -939,7 +948,7 @@ def mla_bwd(q, kv, k_rope, o, lse, d_o, cu_seqlens_q=None, cu_seqlens_k=None, ca
             _need(dk_rope, "dk_rope", (B, Tk, Dr), dt, dev)
     workspace = _workspace(workspace, mla_bwd_workspace_bytes(B, Tq, Tk, H, Dr), dev)
     row, batch = _steps(k_rope, 1, 0)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib.kda_mla_bwd(_ptr(q), _ptr(kv), _ptr(k_rope), row, batch, _ptr(cu_seqlens_q), _ptr(cu_seqlens_k),
                                _ptr(o), _ptr(lse), _ptr(d_o), B, Tq, Tk, H, Dn, Dr, N, int(bool(causal)), scale,
                                _DTYPES[dt], int(rest), _ptr(workspace), workspace.numel(), _ptr(dq), _ptr(dkv),
@@ -989,7 +998,7 @@ def mla_cache_append(latent, k_rope, cache, page_table, cache_lens, cu_seqlens=N
         raise ValueError(f"cache rows have {D} channels, latent and k_rope {Dc + Dr}")
     lrow, lbatch = _steps(latent, 1, 0)
     krow, kbatch = _steps(k_rope, 1, 0)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib.kda_mla_cache_append(_ptr(latent), lrow, lbatch, _ptr(k_rope), krow, kbatch, _ptr(cache),
                                         _ptr(page_table), _ptr(cache_lens), _ptr(cu_seqlens), n_pages, page_size,
                                         max_pages, B, T, Dc, Dr, N, _DTYPES[dt], _stream(dev)))
@@ -1035,7 +1044,7 @@ def mla_step(q_latent, q_rope, cache, page_table, seq_lens, scale, out=None, lse
     else:
         _need(lse, "lse", (Nb, Tq, H), torch.float32, dev)
     workspace = _workspace(workspace, mla_step_workspace_bytes(Nb, Tq, H, Dc, page_size, max_pages, dt), dev)
-    with torch.cuda.device(dev):
+    with _on(dev):
         _check(lib.kda_mla_step(_ptr(q_latent), *_steps(q_latent, 0, 1, 2), _ptr(q_rope), *_steps(q_rope, 0, 1, 2),
                                 _ptr(cache), _ptr(page_table), _ptr(seq_lens), n_pages, page_size, max_pages, Nb, Tq,
                                 H, Dc, Dr, float(scale), _DTYPES[dt], _ptr(workspace), workspace.numel(), _ptr(out),

@@ -76,6 +76,11 @@ __device__ __forceinline__ void load_lds16(const char* g, char* lds) {
     const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(KDA_LDS char*)lds);
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(base), "v"(g) : "memory");
 }
+// the same from g (uniform) + off bytes
+__device__ __forceinline__ void load_lds16s(const char* g, int off, char* lds) {
+    const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(KDA_LDS char*)lds);
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(base), "v"(off), "s"(g) : "memory");
+}
 
 // Rows [0, ROWS) of a tile from global rows g + r * stride bytes (r clamped
 // to rmax) to LDS, NT threads (wave w, uniform), not waited for. ROWS * RC is a multiple of NT.

@@ -92,7 +92,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
         if constexpr (DR > 0) load_tile<CR, BN, 256>(buf + 2 * kK, krp + k0 * krs, krs, rmax, w, lane);
     };
     if (tiles > 0) load(0, smem[0]);
-    wait_loads();
+    wait_loads_and_lds();
     wg_barrier();
     for (int t = 0; t < tiles; ++t) {
         const char* buf = smem[t & 1];
@@ -139,7 +139,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
                 }
             }
         }
-        wait_loads();
+        wait_loads_and_lds();
         wg_barrier();
     }
     T* p = static_cast<T*>(a.dq) + qrow * DQ;
@@ -225,8 +225,7 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
         load_stat(0, x);
         put_stat(0, x);
     }
-    wait_loads();
-    __builtin_amdgcn_s_waitcnt(0xC07F);
+    wait_loads_and_lds();
     wg_barrier();
     for (int t = 0; t < tiles; ++t) {
         const char* buf = smem[t & 1];
@@ -277,8 +276,7 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
             }
         }
         if (t + 1 < tiles) put_stat((t + 1) & 1, x);
-        wait_loads();
-        __builtin_amdgcn_s_waitcnt(0xC07F);                // lgkmcnt(0): the row statistics are in LDS
+        wait_loads_and_lds();
         wg_barrier();
     }
     const bool live = j < Lk;

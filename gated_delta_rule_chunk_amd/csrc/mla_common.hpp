@@ -79,7 +79,10 @@ __device__ __forceinline__ void load_lds16(const char* g, char* lds) {
 // the same from g (uniform) + off bytes
 __device__ __forceinline__ void load_lds16s(const char* g, int off, char* lds) {
     const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(KDA_LDS char*)lds);
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(base), "v"(off), "s"(g) : "memory");
+    const uint64_t u = reinterpret_cast<uint64_t>(g);
+    const uint64_t from = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32 |
+                          (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u);
+    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(base), "v"(off), "s"(from) : "memory");
 }
 
 // Rows [0, ROWS) of a tile from global rows g + r * stride bytes (r clamped
@@ -210,15 +213,17 @@ __device__ __forceinline__ void store_tile(T* p, const f32x16& acc, float mul, i
 }
 
 // The workgroup barrier without a fence: every wave has waited for its own
-// loads into LDS and consumed its own reads before it.
+// loads and LDS accesses before it (wait_loads_and_lds).
 __device__ __forceinline__ void wg_barrier() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
 }
-__device__ __forceinline__ void wait_loads() {
+// Waits for this wave's loads into LDS and for its own LDS accesses. (The
+// builtin, so that the compiler knows of it.)
+__device__ __forceinline__ void wait_loads_and_lds() {
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_waitcnt(0x0F70);   // vmcnt(0); the builtin, so that the compiler knows of it
+    __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0)
     asm volatile("" ::: "memory");
 }
 

@@ -81,7 +81,7 @@ __global__ __launch_bounds__(256, QB == 1 && sizeof(T) == 2 ? 2 : 1) void mla_fw
         if constexpr (DR > 0) load_tile<CR, BN, 256>(buf + 2 * kK, krp + k0 * krs, krs, rmax, w, lane);
     };
     if (tiles > 0) load(0, smem[0]);
-    wait_loads();
+    wait_loads_and_lds();
     wg_barrier();
     for (int t = 0; t < tiles; ++t) {
         const char* buf = smem[t & 1];
@@ -168,7 +168,7 @@ __global__ __launch_bounds__(256, QB == 1 && sizeof(T) == 2 ? 2 : 1) void mla_fw
                     }
                 }
         }
-        wait_loads();
+        wait_loads_and_lds();
         wg_barrier();
     }
     T* op = static_cast<T*>(a.o);

@@ -72,12 +72,15 @@ __device__ __forceinline__ float* partial(const MlaStepArgs& a, int group, int p
 }
 
 // A tile's 32 rows of RC chunks to LDS (layout: mla_common.hpp). Rows 0-15 lie
-// at lo and 16-31 at hi, 16 consecutive rows each; with CLAMP, rows past rmax
-// are not read (row rmax stands in). Lane l of instruction i fills chunk
-// 64 i + l of the tile; as a row's chunks are permuted within their groups
-// only, its source is that chunk with its low bits exchanged.
-template <int RC, int WAVES, bool CLAMP>
-__device__ __forceinline__ void load_cache_tile(char* lds, const char* lo, const char* hi, int rmax, int w, int lane) {
+// at lo and 16-31 at hi, 16 consecutive rows each. Lane l of instruction i
+// fills chunk 64 i + l of the tile; as a row's chunks are permuted within
+// their groups only, its source is that chunk with its low bits exchanged.
+// With EDGE, rows past rmax are not read (row rmax stands in), and halves
+// whose page does not exist (bits of have) are zeros: a hidden row's weight is
+// 0, but what it multiplies has to be finite.
+template <int RC, int WAVES, bool EDGE>
+__device__ __forceinline__ void load_cache_tile(char* lds, const char* lo, const char* hi, int rmax, int have, int w,
+                                                int lane) {
     constexpr int kInstr = kTile * RC / 64, kHalf = kInstr / 2;
     asm volatile("" : "+v"(lane));   // addresses are formed here for each tile, not kept in registers
 #pragma unroll
@@ -85,25 +88,23 @@ __device__ __forceinline__ void load_cache_tile(char* lds, const char* lo, const
         const int i = k * WAVES + w;
         if (kInstr % WAVES != 0 && i >= kInstr) break;
         const int s = i * 64 + lane;
-        int r, src;
+        int r;
         if constexpr (RC % 64 == 0) {                     // an instruction stays in one row
             r = i / (RC / 64);
-            src = s ^ swizzle<RC>(r);
-        } else {
-            constexpr int U = RC / 8;                     // a row has U groups of 8 chunks
-            const unsigned x = 8u * (unsigned)i + ((unsigned)lane >> 3);
-            r = (int)(x / (unsigned)U);
-            src = s ^ swizzle<RC>(r);
+        } else {                                          // a row has RC / 8 groups of 8 chunks
+            r = (int)((8u * (unsigned)i + ((unsigned)lane >> 3)) / (unsigned)(RC / 8));
         }
-        const bool second = i >= kHalf;
-        if constexpr (CLAMP) {
-            if (r > rmax) src -= (r - rmax) * RC;
-            // rmax < 16 may send a lane of the second half back to the first
-            const bool back = second && rmax < 16;
-            const char* base = second && !back ? hi : lo;
-            load_lds16(base + (int64_t)(second && !back ? src - 16 * RC : src) * 16, lds + i * 1024);
+        const int src = s ^ swizzle<RC>(r);
+        if constexpr (EDGE) {
+            const int half = i >= kHalf && rmax >= 16;    // where its rows come from
+            if (have >> half & 1) {
+                const int rr = r > rmax ? rmax : r;
+                load_lds16((rr < 16 ? lo : hi - 16 * RC * 16) + (src + (rr - r) * RC) * 16, lds + i * 1024);
+            } else {
+                *reinterpret_cast<u32x4*>(lds + i * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
+            }
         } else {
-            load_lds16s((second ? hi - 16 * RC * 16 : lo), src * 16, lds + i * 1024);
+            load_lds16s((i >= kHalf ? hi - 16 * RC * 16 : lo), src * 16, lds + i * 1024);
         }
     }
 }
@@ -173,8 +174,10 @@ __global__ __launch_bounds__(128 * BLK, BLK > 2 ? 2 : 1) void mla_step_kernel(Ml
                 const int i = p + lane;
                 int e = i < a.max_pages ? table[i] : -1;
                 if (e < 0 || e >= a.n_pages) e = -1;
-                const uint64_t bad = __ballot(i <= (len - 1) >> ps && e < 0);
-                if (bad && w == 0 && lane == 0) atomicAdd(a.status, (unsigned)__popcll(bad));
+                // counted once: where the page's first row is this part's
+                const int64_t r = (int64_t)i << ps;
+                const uint64_t bad = __ballot(e < 0 && r < len && r >= t0 * kTile && r < (int64_t)t1 * kTile);
+                if (bad && group == 0 && w == 0 && lane == 0) atomicAdd(a.status, (unsigned)__popcll(bad));
                 pages = e;
             }
             return __builtin_amdgcn_readlane(pages, p - pbase);
@@ -195,12 +198,13 @@ __global__ __launch_bounds__(128 * BLK, BLK > 2 ? 2 : 1) void mla_step_kernel(Ml
             }
             const char* lo = static_cast<const char*>(a.cache) + r0 * (RC * 16);
             const char* hi = static_cast<const char*>(a.cache) + r1 * (RC * 16);
-            if (k0 + kTile <= len) load_cache_tile<RC, WAVES, false>(buf, lo, hi, 0, w, lane);
-            else load_cache_tile<RC, WAVES, true>(buf, lo, hi, len - 1 - k0, w, lane);
-            return (e0 >= 0) | (e1 >= 0) << 1;
+            const int have = (e0 >= 0) | (e1 >= 0) << 1;
+            if (have == 3 && k0 + kTile <= len) load_cache_tile<RC, WAVES, false>(buf, lo, hi, 0, 0, w, lane);
+            else load_cache_tile<RC, WAVES, true>(buf, lo, hi, len - 1 - k0, have, w, lane);
+            return have;
         };
         int have = load(t0, smem[0]), next_have = 0;
-        wait_loads();
+        wait_loads_and_lds();
         wg_barrier();
         for (int t = t0; t < t1; ++t) {
             const char* buf = smem[(t - t0) & 1];
@@ -267,7 +271,7 @@ __global__ __launch_bounds__(128 * BLK, BLK > 2 ? 2 : 1) void mla_step_kernel(Ml
                     acc[d] = mma(read_cols<T, RC>(buf + half * (DC / 2) * sizeof(T), 16 * s, 32 * d, lane), pf, acc[d]);
             }
             have = next_have;
-            wait_loads();
+            wait_loads_and_lds();
             wg_barrier();
         }
         const float lt = half_sum(lsum);

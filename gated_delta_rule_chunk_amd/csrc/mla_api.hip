@@ -69,8 +69,12 @@ kda_status check_expanded(const char* fn, const void* q, const void* kv, const v
         return fail(KDA_ERR_INVALID_ARG, "%s: q, kv and k_rope must be 16-byte aligned", fn);
     // the kernels count workgroups in 31 bits
     const int64_t rows = (Tq > Tk ? Tq : Tk) / 128 + 1;
-    if (((int64_t)(cuq ? 1 : B) * rows + N) * H > ((int64_t)1 << 30) || H > (1 << 20))
+    if (((int64_t)(cuq ? 1 : B) * rows + N) * H > ((int64_t)1 << 30))
         return fail(KDA_ERR_UNSUPPORTED, "%s: problem too large", fn);
+    // and the bytes of a tile's 64 rows in 31
+    if (H > 4096 || (Dr && kr_row > (1 << 22)))
+        return fail(KDA_ERR_UNSUPPORTED, "%s: H=%d, k_rope row stride %lld; at most 4096 and 2^22 elements", fn, H,
+                    (long long)kr_row);
     a.q = q; a.kv = kv; a.kr = k_rope; a.kr_row = kr_row; a.kr_batch = kr_batch; a.cuq = cuq; a.cuk = cuk;
     a.B = B; a.Tq = Tq; a.Tk = Tk; a.H = H; a.Dn = Dn; a.Dr = Dr; a.N = N;
     a.causal = causal != 0; a.bf16 = dtype == KDA_BF16; a.zero_rest = zero_rest != 0; a.scale = scale;

@@ -85,11 +85,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
     // a row without a visible key has lse -inf; all its terms are hidden below
     const float lse = rest ? 0.f : a.lse[srow], l2 = lse == -INFINITY ? 0.f : lse * kLog2e;
 
+    TileLoad<CK, BN, 4> lk;
+    TileLoad<DR ? CR : 8, BN, 4> lr;
+    lk.init(kvs, w, lane);
+    if constexpr (DR > 0) lr.init(krs, w, lane);
     auto load = [&](int t, char* buf) {
         const int k0 = t * BN, rmax = Lk - 1 - k0;
-        load_tile<CK, BN, 256>(buf, kvp + k0 * kvs, kvs, rmax, w, lane);
-        load_tile<CK, BN, 256>(buf + kK, kvp + DN * sizeof(T) + k0 * kvs, kvs, rmax, w, lane);
-        if constexpr (DR > 0) load_tile<CR, BN, 256>(buf + 2 * kK, krp + k0 * krs, krs, rmax, w, lane);
+        lk.load(buf, kvp + k0 * kvs, kvs, rmax, w, lane);
+        lk.load(buf + kK, kvp + DN * sizeof(T) + k0 * kvs, kvs, rmax, w, lane);
+        if constexpr (DR > 0) lr.load(buf + 2 * kK, krp + k0 * krs, krs, rmax, w, lane);
     };
     if (tiles > 0) load(0, smem[0]);
     wait_loads_and_lds();
@@ -111,11 +115,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
                     sc = mma(read_rows<T, CR>(buf + 2 * kK, 32 * kb + n32, s - DN / 16, hf), qf[s], sc);
                 }
             }
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r], c, -l2));
-                sc[r] = p * (dp[r] - delta);
-            }
+            if constexpr (sizeof(T) == 2) sched_reads_under_mma<6, 1, (DQ + DN) / 16 - 6>();
             if (k0 + 32 > Lk || (a.causal && k0 + 31 > wq0 + off)) {
                 int lim = Lk - 1 - k0;
                 if (a.causal) {
@@ -124,7 +124,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
                 }
                 lim -= 4 * hf;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) sc[r] = 8 * (r / 4) + r % 4 > lim ? 0.f : sc[r];
+                for (int r = 0; r < 16; ++r) sc[r] = 8 * (r / 4) + r % 4 > lim ? -INFINITY : sc[r];
+            }
+#pragma unroll
+            for (int r = 0; r < 16; ++r) {
+                const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r], c, -l2));
+                sc[r] = p * (dp[r] - delta);
             }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
@@ -138,6 +143,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
                     }
                 }
             }
+            if constexpr (sizeof(T) == 2) sched_reads_over_valu<8, 90, 2, DQ / 16 - 4>();
         }
         wait_loads_and_lds();
         wg_barrier();
@@ -150,8 +156,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
 template <class T, int DN, int DR>
 __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slots) {
     constexpr int DQ = DN + DR, BQ = kBwdRows<T>, QB = BQ / 32, BK = 128;
-    constexpr int CQ = DQ / kChunk<T>, CO = DN / kChunk<T>;
-    constexpr int kQ = BQ * CQ * 16, kBuf = kQ + BQ * CO * 16;
+    constexpr int CN = DN / kChunk<T>, CR = DR / kChunk<T>;
+    constexpr int kQ = BQ * CN * 16, kBuf = 2 * kQ + BQ * CR * 16;    // q's own part, d_o, q's shared part
     __shared__ __attribute__((aligned(1024))) char smem[2][kBuf];
     __shared__ __attribute__((aligned(16))) float stat[2][2][BQ];     // lse (base 2) and D of the tile's rows
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -200,10 +206,16 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
     const char* dp_ = static_cast<const char*>(a.d_o) + (qs * a.H + h) * DN * (int64_t)sizeof(T);
     const int64_t srow = ((a.cuq ? 0 : (int64_t)n * a.H) + h) * a.Tq + (a.cuq ? qs : 0);
 
+    TileLoad<CN, BQ, 4> lq, ld;
+    TileLoad<DR ? CR : 8, BQ, 4> lr;
+    lq.init(qst, w, lane);
+    ld.init(ost, w, lane);
+    if constexpr (DR > 0) lr.init(qst, w, lane);
     auto load = [&](int t, char* buf) {
         const int r0 = first + t * BQ, rmax = Lq - 1 - r0;
-        load_tile<CQ, BQ, 256>(buf, qp + r0 * qst, qst, rmax, w, lane);
-        load_tile<CO, BQ, 256>(buf + kQ, dp_ + r0 * ost, ost, rmax, w, lane);
+        lq.load(buf, qp + r0 * qst, qst, rmax, w, lane);
+        ld.load(buf + kQ, dp_ + r0 * ost, ost, rmax, w, lane);
+        if constexpr (DR > 0) lr.load(buf + 2 * kQ, qp + DN * sizeof(T) + r0 * qst, qst, rmax, w, lane);
     };
     // Rows past the sequence and rows without a visible key get lse = +inf,
     // which makes all their terms zero.
@@ -240,9 +252,18 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
             f32x16 sc = zero16(), dp = zero16();
 #pragma unroll
             for (int s = 0; s < DQ / 16; ++s) {
-                sc = mma(read_rows<T, CQ>(buf, 32 * qb + n32, s, hf), kf[s], sc);
-                if (s < DN / 16)
-                    dp = mma(read_rows<T, CO>(buf + kQ, 32 * qb + n32, s, hf), vf[s < DN / 16 ? s : 0], dp);
+                if (s < DN / 16) {
+                    sc = mma(read_rows<T, CN>(buf, 32 * qb + n32, s, hf), kf[s], sc);
+                    dp = mma(read_rows<T, CN>(buf + kQ, 32 * qb + n32, s, hf), vf[s < DN / 16 ? s : 0], dp);
+                } else if constexpr (DR > 0) {
+                    sc = mma(read_rows<T, CR>(buf + 2 * kQ, 32 * qb + n32, s - DN / 16, hf), kf[s], sc);
+                }
+            }
+            if constexpr (sizeof(T) == 2) sched_reads_under_mma<6, 1, (DQ + DN) / 16 - 6>();
+            if (a.causal && wk0 + 31 > r0 + off) {
+                const int lim = j - off - r0 - 4 * hf;     // rows below it do not see this lane's key
+#pragma unroll
+                for (int r = 0; r < 16; ++r) sc[r] = 8 * (r / 4) + r % 4 < lim ? -INFINITY : sc[r];
             }
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
@@ -255,25 +276,22 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
                     dp[r] = sc[r] * (dp[r] - de[e]);
                 }
             }
-            if (a.causal && wk0 + 31 > r0 + off) {
-                const int lim = j - off - r0 - 4 * hf;     // rows below it do not see this lane's key
-#pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const bool hide = 8 * (r / 4) + r % 4 < lim;
-                    sc[r] = hide ? 0.f : sc[r];
-                    dp[r] = hide ? 0.f : dp[r];
-                }
-            }
 #pragma unroll
             for (int s = 0; s < 2; ++s) {
                 const Frag<T> pf = to_frag<T>(sc, s), sf = to_frag<T>(dp, s);
 #pragma unroll
                 for (int d = 0; d < DN / 32; ++d)
-                    dv[d] = mma(read_cols<T, CO>(buf + kQ, 32 * qb + 16 * s, 32 * d, lane), pf, dv[d]);
+                    dv[d] = mma(read_cols<T, CN>(buf + kQ, 32 * qb + 16 * s, 32 * d, lane), pf, dv[d]);
 #pragma unroll
-                for (int d = 0; d < DQ / 32; ++d)
-                    dk[d] = mma(read_cols<T, CQ>(buf, 32 * qb + 16 * s, 32 * d, lane), sf, dk[d]);
+                for (int d = 0; d < DQ / 32; ++d) {
+                    if (d < DN / 32) {
+                        dk[d] = mma(read_cols<T, CN>(buf, 32 * qb + 16 * s, 32 * d, lane), sf, dk[d]);
+                    } else if constexpr (DR > 0) {
+                        dk[d] = mma(read_cols<T, CR>(buf + 2 * kQ, 32 * qb + 16 * s, 32 * d - DN, lane), sf, dk[d]);
+                    }
+                }
             }
+            if constexpr (sizeof(T) == 2) sched_reads_over_valu<16, 110, 2, (DQ + DN) / 16 - 4>();
         }
         if (t + 1 < tiles) put_stat((t + 1) & 1, x);
         wait_loads_and_lds();

@@ -85,17 +85,65 @@ __device__ __forceinline__ void load_lds16s(const char* g, int off, char* lds) {
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(base), "v"(off), "s"(from) : "memory");
 }
 
-// Rows [0, ROWS) of a tile from global rows g + r * stride bytes (r clamped
-// to rmax) to LDS, NT threads (wave w, uniform), not waited for. ROWS * RC is a multiple of NT.
-template <int RC, int ROWS, int NT>
-__device__ __forceinline__ void load_tile(char* lds, const char* g, int64_t stride, int rmax, int w, int lane) {
-    static_assert(ROWS * RC % NT == 0 && NT % 64 == 0, "whole instructions");
+// Rows [0, ROWS) of a tile from global rows `stride` bytes apart to LDS, WAVES
+// waves (this one w), not waited for. Each instruction covers 64 / RC (or a
+// part of) rows; the swizzle repeats every 16 rows, so a lane's offset in the
+// tile takes P values only, kept in registers, and the row of an instruction
+// goes into the uniform base: no vector arithmetic per tile.
+template <int RC, int ROWS, int WAVES> struct TileLoad {
+    static constexpr int NT = 64 * WAVES, kInstr = ROWS * RC / NT;
+    static_assert(ROWS * RC % NT == 0 && NT % RC == 0, "whole rows an instruction of all waves");
+    static constexpr int R = NT / RC;                     // rows an instruction of all waves
+    static constexpr int P = R >= 16 ? 1 : 16 / R < kInstr ? 16 / R : kInstr;
+    int off[P];
+
+    __device__ __forceinline__ void init(int64_t stride, int w, int lane) {
+        const int s = w * 64 + lane;
 #pragma unroll
-    for (int i = 0; i < ROWS * RC / NT; ++i) {
-        const int s = i * NT + w * 64 + lane;
-        const int r = s / RC, c = (s % RC) ^ swizzle<RC>(r);
-        const int rr = r < rmax ? r : rmax;
-        load_lds16(g + rr * stride + c * 16, lds + (i * NT + w * 64) * 16);
+        for (int i = 0; i < P; ++i) off[i] = (s / RC) * (int)stride + (((s % RC) ^ swizzle<RC>(i * R + s / RC)) << 4);
+    }
+    // all rows exist
+    __device__ __forceinline__ void full(char* lds, const char* g, int64_t stride, int w) const {
+#pragma unroll
+        for (int i = 0; i < kInstr; ++i) load_lds16s(g + i * R * stride, off[i % P], lds + (i * NT + w * 64) * 16);
+    }
+    // rows past rmax are not read: row rmax stands in
+    __device__ __forceinline__ void edge(char* lds, const char* g, int64_t stride, int rmax, int w, int lane) const {
+        asm volatile("" : "+v"(lane));                    // nothing of this is kept over the tiles
+        const int s = w * 64 + lane;
+#pragma unroll
+        for (int i = 0; i < kInstr; ++i) {
+            const int r = i * R + s / RC, rr = r < rmax ? r : rmax;
+            load_lds16(g + rr * stride + (((s % RC) ^ swizzle<RC>(r)) << 4), lds + (i * NT + w * 64) * 16);
+        }
+    }
+    __device__ __forceinline__ void load(char* lds, const char* g, int64_t stride, int rmax, int w, int lane) const {
+        if (rmax >= ROWS - 1) full(lds, g, stride, w);
+        else edge(lds, g, stride, rmax, w, lane);
+    }
+};
+
+// Scheduling: AHEAD LDS reads first, then EACH reads after every one of MMAS
+// matrix instructions, so that operands are under way while the ones before
+// them are used.
+template <int AHEAD, int EACH, int MMAS> __device__ __forceinline__ void sched_reads_under_mma() {
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 0);
+#pragma unroll
+    for (int i = 0; i < MMAS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+        __builtin_amdgcn_sched_group_barrier(0x100, EACH, 0);
+    }
+}
+
+// The same where vector arithmetic (about VALU instructions) comes between the
+// first reads and the products that use them.
+template <int AHEAD, int VALU, int EACH, int MMAS> __device__ __forceinline__ void sched_reads_over_valu() {
+    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 1);
+    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 1);
+#pragma unroll
+    for (int i = 0; i < MMAS; ++i) {
+        __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
+        __builtin_amdgcn_sched_group_barrier(0x100, EACH, 1);
     }
 }
 

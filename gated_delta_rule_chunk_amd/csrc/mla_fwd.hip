@@ -74,22 +74,21 @@ __global__ __launch_bounds__(256, QB == 1 && sizeof(T) == 2 ? 2 : 1) void mla_fw
     }
     const float c = a.scale * kLog2e;
 
+    TileLoad<CK, BN, 4> lk;
+    TileLoad<DR ? CR : 8, BN, 4> lr;
+    lk.init(kvs, w, lane);
+    if constexpr (DR > 0) lr.init(krs, w, lane);
     auto load = [&](int t, char* buf) {
         const int k0 = t * BN, rmax = Lk - 1 - k0;
-        load_tile<CK, BN, 256>(buf, kvp + k0 * kvs, kvs, rmax, w, lane);
-        load_tile<CK, BN, 256>(buf + kK, kvp + DN * sizeof(T) + k0 * kvs, kvs, rmax, w, lane);
-        if constexpr (DR > 0) load_tile<CR, BN, 256>(buf + 2 * kK, krp + k0 * krs, krs, rmax, w, lane);
+        lk.load(buf, kvp + k0 * kvs, kvs, rmax, w, lane);
+        lk.load(buf + kK, kvp + DN * sizeof(T) + k0 * kvs, kvs, rmax, w, lane);
+        if constexpr (DR > 0) lr.load(buf + 2 * kK, krp + k0 * krs, krs, rmax, w, lane);
     };
-    if (tiles > 0) load(0, smem[0]);
-    wait_loads_and_lds();
-    wg_barrier();
-    for (int t = 0; t < tiles; ++t) {
-        const char* buf = smem[t & 1];
-        if (t + 1 < tiles) load(t + 1, smem[(t + 1) & 1]);
+    auto tile_step = [&](int t, const char* buf, char* next) {
+        if (t + 1 < tiles) load(t + 1, next);
         const int k0 = t * BN;
         // rows of this wave all before the tile's first key: nothing to do
-        const bool any = !a.causal || k0 <= wq0 + 32 * QB - 1 + off;
-        if (any) {
+        if (!a.causal || k0 <= wq0 + 32 * QB - 1 + off) {
             f32x16 sc[QB][KB];
 #pragma unroll
             for (int b = 0; b < QB; ++b)
@@ -108,6 +107,7 @@ __global__ __launch_bounds__(256, QB == 1 && sizeof(T) == 2 ? 2 : 1) void mla_fw
 #pragma unroll
                     for (int b = 0; b < QB; ++b) sc[b][kb] = mma(kf, qf[b][s], sc[b][kb]);
                 }
+            if constexpr (sizeof(T) == 2) sched_reads_under_mma<6, 1, DQ / 16 * KB - 6>();
             // hide keys past the sequence or after the row
             if (k0 + BN > Lk || (a.causal && k0 + BN - 1 > wq0 + off)) {
 #pragma unroll
@@ -125,32 +125,49 @@ __global__ __launch_bounds__(256, QB == 1 && sizeof(T) == 2 ? 2 : 1) void mla_fw
                             sc[b][kb][r] = 32 * kb + 8 * (r / 4) + r % 4 > lim ? -INFINITY : sc[b][kb][r];
                 }
             }
+            float mx[QB];
+            bool grown = false;
 #pragma unroll
             for (int b = 0; b < QB; ++b) {
-                float mx = sc[b][0][0];
+                mx[b] = sc[b][0][0];
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) mx = fmaxf(mx, sc[b][kb][r]);
-                mx = half_max(mx);
-                const float mn = fmaxf(m[b], mx);
-                const float ms = mn == -INFINITY ? 0.f : mn;          // nothing seen yet: all terms are 0
-                const float al = __builtin_amdgcn_exp2f((m[b] - ms) * c);
+                    for (int r = 0; r < 16; ++r) mx[b] = fmaxf(mx[b], sc[b][kb][r]);
+                mx[b] = half_max(mx[b]);
+                grown |= (mx[b] - m[b]) * c > 8.f;
+            }
+            // The running maximum moves only when some row's grows by more
+            // than 2^8 (from -inf at first): until then its terms reach at
+            // most 2^8, exact enough in float32, and the output needs no
+            // rescaling.
+            if (__any(grown)) {
+#pragma unroll
+                for (int b = 0; b < QB; ++b) {
+                    const float mn = fmaxf(m[b], mx[b]);
+                    const float ms = mn == -INFINITY ? 0.f : mn;      // nothing seen yet: all terms are 0
+                    const float al = __builtin_amdgcn_exp2f((m[b] - ms) * c);
+                    l[b] *= al;
+                    m[b] = mn;
+#pragma unroll
+                    for (int d = 0; d < DN / 32; ++d)
+#pragma unroll
+                        for (int r = 0; r < 16; ++r) acc[b][d][r] *= al;
+                }
+            }
+#pragma unroll
+            for (int b = 0; b < QB; ++b) {
+                const float mc = m[b] == -INFINITY ? 0.f : m[b] * c;
                 float sum = 0.f;
 #pragma unroll
                 for (int kb = 0; kb < KB; ++kb)
 #pragma unroll
                     for (int r = 0; r < 16; ++r) {
-                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][kb][r], c, -ms * c));
+                        const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[b][kb][r], c, -mc));
                         sc[b][kb][r] = p;
                         sum += p;
                     }
-                l[b] = l[b] * al + sum;
-                m[b] = mn;
-#pragma unroll
-                for (int d = 0; d < DN / 32; ++d)
-#pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[b][d][r] *= al;
+                l[b] += sum;
             }
             const char* vb = buf + kK;
 #pragma unroll
@@ -170,6 +187,13 @@ __global__ __launch_bounds__(256, QB == 1 && sizeof(T) == 2 ? 2 : 1) void mla_fw
         }
         wait_loads_and_lds();
         wg_barrier();
+    };
+    if (tiles > 0) load(0, smem[0]);
+    wait_loads_and_lds();
+    wg_barrier();
+    for (int t = 0; t < tiles; t += 2) {
+        tile_step(t, smem[0], smem[1]);
+        if (t + 1 < tiles) tile_step(t + 1, smem[1], smem[0]);
     }
     T* op = static_cast<T*>(a.o);
 #pragma unroll

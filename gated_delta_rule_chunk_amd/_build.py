@@ -17,20 +17,23 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["kda_api.hip", "chunk_mfma.hip", "chunk_generic.hip", "chunk_bwd.hip", "recurrent_step.hip",
            "short_conv.hip", "split.hip", "prologue_bwd.hip", "mla_api.hip", "mla_fwd.hip", "mla_bwd.hip",
-           "mla_step.hip"]
+           "mla_dkv_bf16.hip", "mla_step.hip"]
 CFLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
     # no packed-fp32 instructions in any generated code
     "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-    # keep matrix-core accumulators in ordinary VGPRs (avoids AGPR copies)
-    "-mllvm", "-amdgpu-mfma-vgpr-form",
     "-I", os.path.join(ROOT, "include"),
 ]
+# keep matrix-core accumulators in ordinary VGPRs (avoids AGPR copies), but for
+# the sources whose accumulators and operands do not fit them together
+VGPR_FORM = ["-mllvm", "-amdgpu-mfma-vgpr-form"]
+AGPR_SOURCES = ["mla_dkv_bf16.hip"]
 
 
 def _compile(src, verbose):
     obj = os.path.join(BUILD_DIR, os.path.splitext(src)[0] + ".o")
-    cmd = [HIPCC] + CFLAGS + ["-c", os.path.join(CSRC, src), "-o", obj]
+    cmd = [HIPCC] + CFLAGS + ([] if src in AGPR_SOURCES else VGPR_FORM) + [
+        "-c", os.path.join(CSRC, src), "-o", obj]
     if verbose:
         print(" ".join(cmd), flush=True)
     r = subprocess.run(cmd, capture_output=True, text=True)

@@ -296,5 +296,6 @@ hipError_t launch_mla_step(const MlaStepArgs& a, hipStream_t stream);
 hipError_t launch_mla_append(const MlaAppendArgs& a, hipStream_t stream);
 hipError_t launch_mla_fwd(const MlaArgs& a, hipStream_t stream);
 hipError_t launch_mla_bwd(const MlaArgs& a, hipStream_t stream);
+hipError_t launch_mla_dkv_bf16(const MlaArgs& a, hipStream_t stream);   // its second kernel
 
 }  // namespace kda

@@ -15,6 +15,7 @@
 // order, from float32 shares. Bound by the matrix cores.
 #include "launchers.hpp"
 #include "mla_common.hpp"
+#include "mla_dkv.hpp"
 
 namespace kda {
 namespace {
@@ -22,7 +23,6 @@ namespace {
 using namespace mla;
 
 template <class T> constexpr int kBwdKeys = sizeof(T) == 2 ? 64 : 32;     // keys a tile (dq)
-template <class T> constexpr int kBwdRows = sizeof(T) == 2 ? 64 : 32;     // queries a tile (dk, dv)
 
 template <class T, int DN, int DR>
 __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(MlaArgs a, int64_t slots) {
@@ -126,24 +126,23 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
 #pragma unroll
                 for (int r = 0; r < 16; ++r) sc[r] = 8 * (r / 4) + r % 4 > lim ? -INFINITY : sc[r];
             }
+            auto read = [&](int i) -> Frag<T> {
+                const int s = i / (DQ / 32), d = i % (DQ / 32);
+                if constexpr (DR > 0)
+                    if (d >= DN / 32) return read_cols<T, CR>(buf + 2 * kK, 32 * kb + 16 * s, 32 * d - DN, lane);
+                return read_cols<T, CK>(buf, 32 * kb + 16 * s, 32 * d, lane);
+            };
+            ReadAhead<T, DQ / 16, 2> ahead;
+            ahead.start(read);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {
                 const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r], c, -l2));
                 sc[r] = p * (dp[r] - delta);
             }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const Frag<T> f = to_frag<T>(sc, s);
-#pragma unroll
-                for (int d = 0; d < DQ / 32; ++d) {
-                    if (d < DN / 32) {
-                        acc[d] = mma(read_cols<T, CK>(buf, 32 * kb + 16 * s, 32 * d, lane), f, acc[d]);
-                    } else if constexpr (DR > 0) {
-                        acc[d] = mma(read_cols<T, CR>(buf + 2 * kK, 32 * kb + 16 * s, 32 * d - DN, lane), f, acc[d]);
-                    }
-                }
-            }
-            if constexpr (sizeof(T) == 2) sched_reads_over_valu<8, 90, 2, DQ / 16 - 4>();
+            const Frag<T> f[2] = {to_frag<T>(sc, 0), to_frag<T>(sc, 1)};
+            ahead.template run<1>(read, [&](int i, const Frag<T>& x) {
+                acc[i % (DQ / 32)] = mma(x, f[i / (DQ / 32)], acc[i % (DQ / 32)]);
+            });
         }
         wait_loads_and_lds();
         wg_barrier();
@@ -151,164 +150,6 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
     T* p = static_cast<T*>(a.dq) + qrow * DQ;
 #pragma unroll
     for (int d = 0; d < DQ / 32; ++d) store_tile<T>(p + 32 * d, acc[d], a.scale, hf, live);
-}
-
-template <class T, int DN, int DR>
-__global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slots) {
-    constexpr int DQ = DN + DR, BQ = kBwdRows<T>, QB = BQ / 32, BK = 128;
-    constexpr int CN = DN / kChunk<T>, CR = DR / kChunk<T>;
-    constexpr int kQ = BQ * CN * 16, kBuf = 2 * kQ + BQ * CR * 16;    // q's own part, d_o, q's shared part
-    __shared__ __attribute__((aligned(1024))) char smem[2][kBuf];
-    __shared__ __attribute__((aligned(16))) float stat[2][2][BQ];     // lse (base 2) and D of the tile's rows
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n32 = lane & 31, hf = lane >> 5;
-    const int64_t item = xcd_item(slots * a.H);
-    if (item < 0) return;
-    const int h = (int)(item / slots);
-    int n, k0, Lq, Lk;
-    int64_t qs, ks;
-    if (!tile_of(a.cuk, a.N, a.Tk, BK, item % slots, lane, n, ks, Lk, k0)) return;
-    const bool rest = a.cuk && n == a.N;
-    if (rest && !a.zero_rest) return;
-    seq_range(a.cuq, a.N, rest ? 0 : n, a.Tq, qs, Lq);
-    if (rest) Lq = 0;
-    const int off = Lk - Lq;
-    const int wk0 = k0 + 32 * w, j = wk0 + n32, jc = j < Lk ? j : Lk - 1;
-    // the first query that sees the block's first key, down to a tile's start
-    int first = 0;
-    if (a.causal && k0 - off > 0) first = (k0 - off) / BQ * BQ;
-    const int tiles = first < Lq ? (Lq - first + BQ - 1) / BQ : 0;
-
-    Frag<T> kf[DQ / 16], vf[DN / 16];
-    const int64_t kvrow = (ks + jc) * a.H + h;
-    {
-        const T* p = static_cast<const T*>(a.kv) + kvrow * 2 * DN + 8 * hf;
-#pragma unroll
-        for (int s = 0; s < DN / 16; ++s) {
-            kf[s] = load8(p + 16 * s);
-            vf[s] = load8(p + DN + 16 * s);
-        }
-        if constexpr (DR > 0) {
-            const T* r = static_cast<const T*>(a.kr) + 8 * hf +
-                         (a.cuk ? (ks + jc) * a.kr_row : n * a.kr_batch + jc * a.kr_row);
-#pragma unroll
-            for (int s = 0; s < DR / 16; ++s) kf[DN / 16 + s] = load8(r + 16 * s);
-        }
-    }
-    f32x16 dk[DQ / 32], dv[DN / 32];
-#pragma unroll
-    for (int d = 0; d < DQ / 32; ++d) dk[d] = zero16();
-#pragma unroll
-    for (int d = 0; d < DN / 32; ++d) dv[d] = zero16();
-    const float c = a.scale * kLog2e;
-    const int64_t qst = (int64_t)a.H * DQ * sizeof(T), ost = (int64_t)a.H * DN * sizeof(T);
-    const char* qp = static_cast<const char*>(a.q) + (qs * a.H + h) * DQ * (int64_t)sizeof(T);
-    const char* dp_ = static_cast<const char*>(a.d_o) + (qs * a.H + h) * DN * (int64_t)sizeof(T);
-    const int64_t srow = ((a.cuq ? 0 : (int64_t)n * a.H) + h) * a.Tq + (a.cuq ? qs : 0);
-
-    TileLoad<CN, BQ, 4> lq, ld;
-    TileLoad<DR ? CR : 8, BQ, 4> lr;
-    lq.init(qst, w, lane);
-    ld.init(ost, w, lane);
-    if constexpr (DR > 0) lr.init(qst, w, lane);
-    auto load = [&](int t, char* buf) {
-        const int r0 = first + t * BQ, rmax = Lq - 1 - r0;
-        lq.load(buf, qp + r0 * qst, qst, rmax, w, lane);
-        ld.load(buf + kQ, dp_ + r0 * ost, ost, rmax, w, lane);
-        if constexpr (DR > 0) lr.load(buf + 2 * kQ, qp + DN * sizeof(T) + r0 * qst, qst, rmax, w, lane);
-    };
-    // Rows past the sequence and rows without a visible key get lse = +inf,
-    // which makes all their terms zero.
-    auto load_stat = [&](int t, float& x) {
-        const int r = first + t * BQ + (threadIdx.x & (BQ - 1));
-        if ((int)threadIdx.x < BQ) {
-            x = r < Lq ? a.lse[srow + r] * kLog2e : INFINITY;
-            if (x == -INFINITY) x = INFINITY;
-        } else if ((int)threadIdx.x < 2 * BQ) {
-            x = r < Lq ? a.delta[srow + r] : 0.f;
-        }
-    };
-    auto put_stat = [&](int b, float x) {
-        if ((int)threadIdx.x < 2 * BQ) stat[b][threadIdx.x / BQ][threadIdx.x % BQ] = x;
-    };
-    float x = 0.f;
-    if (tiles > 0) {
-        load(0, smem[0]);
-        load_stat(0, x);
-        put_stat(0, x);
-    }
-    wait_loads_and_lds();
-    wg_barrier();
-    for (int t = 0; t < tiles; ++t) {
-        const char* buf = smem[t & 1];
-        if (t + 1 < tiles) {
-            load_stat(t + 1, x);
-            load(t + 1, smem[(t + 1) & 1]);
-        }
-#pragma unroll
-        for (int qb = 0; qb < QB; ++qb) {
-            const int r0 = first + t * BQ + 32 * qb;       // query r0 sees keys <= r0 + off
-            if (a.causal && wk0 > r0 + 31 + off) continue;
-            f32x16 sc = zero16(), dp = zero16();
-#pragma unroll
-            for (int s = 0; s < DQ / 16; ++s) {
-                if (s < DN / 16) {
-                    sc = mma(read_rows<T, CN>(buf, 32 * qb + n32, s, hf), kf[s], sc);
-                    dp = mma(read_rows<T, CN>(buf + kQ, 32 * qb + n32, s, hf), vf[s < DN / 16 ? s : 0], dp);
-                } else if constexpr (DR > 0) {
-                    sc = mma(read_rows<T, CR>(buf + 2 * kQ, 32 * qb + n32, s - DN / 16, hf), kf[s], sc);
-                }
-            }
-            if constexpr (sizeof(T) == 2) sched_reads_under_mma<6, 1, (DQ + DN) / 16 - 6>();
-            if (a.causal && wk0 + 31 > r0 + off) {
-                const int lim = j - off - r0 - 4 * hf;     // rows below it do not see this lane's key
-#pragma unroll
-                for (int r = 0; r < 16; ++r) sc[r] = 8 * (r / 4) + r % 4 < lim ? -INFINITY : sc[r];
-            }
-#pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const f32x4 l2 = *reinterpret_cast<const f32x4*>(&stat[t & 1][0][32 * qb + 8 * g + 4 * hf]);
-                const f32x4 de = *reinterpret_cast<const f32x4*>(&stat[t & 1][1][32 * qb + 8 * g + 4 * hf]);
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const int r = 4 * g + e;
-                    sc[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r], c, -l2[e]));
-                    dp[r] = sc[r] * (dp[r] - de[e]);
-                }
-            }
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const Frag<T> pf = to_frag<T>(sc, s), sf = to_frag<T>(dp, s);
-#pragma unroll
-                for (int d = 0; d < DN / 32; ++d)
-                    dv[d] = mma(read_cols<T, CN>(buf + kQ, 32 * qb + 16 * s, 32 * d, lane), pf, dv[d]);
-#pragma unroll
-                for (int d = 0; d < DQ / 32; ++d) {
-                    if (d < DN / 32) {
-                        dk[d] = mma(read_cols<T, CN>(buf, 32 * qb + 16 * s, 32 * d, lane), sf, dk[d]);
-                    } else if constexpr (DR > 0) {
-                        dk[d] = mma(read_cols<T, CR>(buf + 2 * kQ, 32 * qb + 16 * s, 32 * d - DN, lane), sf, dk[d]);
-                    }
-                }
-            }
-            if constexpr (sizeof(T) == 2) sched_reads_over_valu<16, 110, 2, (DQ + DN) / 16 - 4>();
-        }
-        if (t + 1 < tiles) put_stat((t + 1) & 1, x);
-        wait_loads_and_lds();
-        wg_barrier();
-    }
-    const bool live = j < Lk;
-    T* p = static_cast<T*>(a.dkv) + kvrow * 2 * DN;
-#pragma unroll
-    for (int d = 0; d < DN / 32; ++d) {
-        store_tile<T>(p + 32 * d, dk[d], a.scale, hf, live);
-        store_tile<T>(p + DN + 32 * d, dv[d], 1.f, hf, live);
-    }
-    if constexpr (DR > 0) {
-        float* r = a.dkr_part + (((int64_t)h * a.B + (a.cuk ? 0 : n)) * a.Tk + (a.cuk ? ks + jc : jc)) * DR;
-#pragma unroll
-        for (int d = 0; d < DR / 32; ++d) store_tile<float>(r + 32 * d, dk[DN / 32 + d], a.scale, hf, live);
-    }
 }
 
 // Sums the shared key part's shares over the heads, in their order: four
@@ -336,33 +177,30 @@ template <class T> __global__ __launch_bounds__(256) void mla_dkr_kernel(MlaArgs
     for (int j = 0; j < 4; ++j) o[j] = (T)sum[j];
 }
 
-template <class T, int DN, int DR> hipError_t launch(const MlaArgs& a, hipStream_t s) {
-    hipError_t e;
-    int64_t slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 128), items = slots * a.H;
-    if (a.Tq > 0) {
-        mla_dq_kernel<T, DN, DR><<<dim3((unsigned)((items + 7) / 8 * 8)), 256, 0, s>>>(a, slots);
-        if ((e = hipGetLastError()) != hipSuccess) return e;
-    }
-    if (a.Tk == 0) return hipSuccess;
-    slots = tile_slots(a.cuk, a.B, a.N, a.Tk, 128), items = slots * a.H;
-    mla_dkv_kernel<T, DN, DR><<<dim3((unsigned)((items + 7) / 8 * 8)), 256, 0, s>>>(a, slots);
-    if ((e = hipGetLastError()) != hipSuccess) return e;
-    if (DR > 0) {
-        const int64_t quads = (int64_t)a.B * a.Tk * DR / 4;
-        mla_dkr_kernel<T><<<dim3((unsigned)((quads + 255) / 256)), 256, 0, s>>>(a, quads);
-        e = hipGetLastError();
-    }
-    return e;
+template <class T, int DN, int DR> hipError_t launch_dq(const MlaArgs& a, hipStream_t s) {
+    if (a.Tq == 0) return hipSuccess;
+    const int64_t slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 128), items = slots * a.H;
+    mla_dq_kernel<T, DN, DR><<<dim3((unsigned)((items + 7) / 8 * 8)), 256, 0, s>>>(a, slots);
+    return hipGetLastError();
 }
-template <class T> hipError_t launch_dims(const MlaArgs& a, hipStream_t s) {
-    if (a.Dn == 128) return a.Dr ? launch<T, 128, 64>(a, s) : launch<T, 128, 0>(a, s);
-    return a.Dr ? launch<T, 64, 64>(a, s) : launch<T, 64, 0>(a, s);
+template <class T> hipError_t launch_dq_dims(const MlaArgs& a, hipStream_t s) {
+    if (a.Dn == 128) return a.Dr ? launch_dq<T, 128, 64>(a, s) : launch_dq<T, 128, 0>(a, s);
+    return a.Dr ? launch_dq<T, 64, 64>(a, s) : launch_dq<T, 64, 0>(a, s);
+}
+template <class T> hipError_t launch_dkr(const MlaArgs& a, hipStream_t s) {
+    const int64_t quads = (int64_t)a.B * a.Tk * a.Dr / 4;
+    if (quads == 0) return hipSuccess;
+    mla_dkr_kernel<T><<<dim3((unsigned)((quads + 255) / 256)), 256, 0, s>>>(a, quads);
+    return hipGetLastError();
 }
 
 }  // namespace
 
 hipError_t launch_mla_bwd(const MlaArgs& a, hipStream_t s) {
-    return a.bf16 ? launch_dims<__bf16>(a, s) : launch_dims<float>(a, s);
+    hipError_t e = a.bf16 ? launch_dq_dims<__bf16>(a, s) : launch_dq_dims<float>(a, s);
+    if (e == hipSuccess) e = a.bf16 ? launch_mla_dkv_bf16(a, s) : launch_dkv_dims<float>(a, s);
+    if (e == hipSuccess) e = a.bf16 ? launch_dkr<__bf16>(a, s) : launch_dkr<float>(a, s);
+    return e;
 }
 
 }  // namespace kda

@@ -135,17 +135,37 @@ template <int AHEAD, int EACH, int MMAS> __device__ __forceinline__ void sched_r
     }
 }
 
-// The same where vector arithmetic (about VALU instructions) comes between the
-// first reads and the products that use them.
-template <int AHEAD, int VALU, int EACH, int MMAS> __device__ __forceinline__ void sched_reads_over_valu() {
-    __builtin_amdgcn_sched_group_barrier(0x100, AHEAD, 1);
-    __builtin_amdgcn_sched_group_barrier(0x002, VALU, 1);
+// Operands that are read from LDS kAhead at a time in front of their products:
+// start() issues the first reads, before the vector arithmetic that the
+// products wait for, and run() multiplies (use(i, operand) for operand i of N)
+// and keeps reading ahead. read(i) is operand i.
+template <class T, int N, int AHEAD> struct ReadAhead {
+    static constexpr int kAhead = sizeof(T) == 2 ? AHEAD : 2;
+    Frag<T> ring[kAhead];
+
+    template <class Read> __device__ __forceinline__ void start(Read read) {
+        static_assert(N >= kAhead, "operands");
 #pragma unroll
-    for (int i = 0; i < MMAS; ++i) {
-        __builtin_amdgcn_sched_group_barrier(0x008, 1, 1);
-        __builtin_amdgcn_sched_group_barrier(0x100, EACH, 1);
+        for (int i = 0; i < kAhead; ++i) ring[i] = read(i);
+        __builtin_amdgcn_sched_barrier(0);
     }
-}
+    template <int MMAS, class Read, class Use> __device__ __forceinline__ void run(Read read, Use use) {
+        __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+        for (int i = 0; i < N; ++i) {
+            use(i, ring[i % kAhead]);
+            if (i + kAhead < N) ring[i % kAhead] = read(i + kAhead);
+        }
+        if constexpr (sizeof(T) == 2) {
+#pragma unroll
+            for (int i = 0; i < N - kAhead; ++i) {
+                __builtin_amdgcn_sched_group_barrier(0x008, MMAS, 0);     // products with one operand
+                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);        // two transposing reads
+            }
+        }
+        __builtin_amdgcn_sched_barrier(0);
+    }
+};
 
 // Byte offset in a row of chunk k + x (k a multiple of 2 known when compiling,
 // x the lane's part, below 8 with k's bits clear) under swizzle sw. Written so

@@ -155,6 +155,12 @@ __global__ __launch_bounds__(256, QB == 1 && sizeof(T) == 2 ? 2 : 1) void mla_fw
                         for (int r = 0; r < 16; ++r) acc[b][d][r] *= al;
                 }
             }
+            const char* vb = buf + kK;
+            auto read = [&](int i) {
+                return read_cols<T, CK>(vb, 16 * (i / (DN / 32)), 32 * (i % (DN / 32)), lane);
+            };
+            ReadAhead<T, KB * DN / 16, 3> ahead;
+            ahead.start(read);
 #pragma unroll
             for (int b = 0; b < QB; ++b) {
                 const float mc = m[b] == -INFINITY ? 0.f : m[b] * c;
@@ -169,21 +175,16 @@ __global__ __launch_bounds__(256, QB == 1 && sizeof(T) == 2 ? 2 : 1) void mla_fw
                     }
                 l[b] += sum;
             }
-            const char* vb = buf + kK;
+            Frag<T> pf[QB][2 * KB];
 #pragma unroll
-            for (int kb = 0; kb < KB; ++kb)
+            for (int b = 0; b < QB; ++b)
 #pragma unroll
-                for (int s = 0; s < 2; ++s) {
-                    Frag<T> pf[QB];
+                for (int s = 0; s < 2 * KB; ++s) pf[b][s] = to_frag<T>(sc[b][s / 2], s % 2);
+            ahead.template run<QB>(read, [&](int i, const Frag<T>& x) {
+                const int s = i / (DN / 32), d = i % (DN / 32);
 #pragma unroll
-                    for (int b = 0; b < QB; ++b) pf[b] = to_frag<T>(sc[b][kb], s);
-#pragma unroll
-                    for (int d = 0; d < DN / 32; ++d) {
-                        const Frag<T> vf = read_cols<T, CK>(vb, 32 * kb + 16 * s, 32 * d, lane);
-#pragma unroll
-                        for (int b = 0; b < QB; ++b) acc[b][d] = mma(vf, pf[b], acc[b][d]);
-                    }
-                }
+                for (int b = 0; b < QB; ++b) acc[b][d] = mma(x, pf[b][s], acc[b][d]);
+            });
         }
         wait_loads_and_lds();
         wg_barrier();

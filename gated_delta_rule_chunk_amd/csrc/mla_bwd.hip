@@ -32,12 +32,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
     __shared__ __attribute__((aligned(1024))) char smem[2][kBuf];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n32 = lane & 31, hf = lane >> 5;
-    const int64_t item = xcd_item(slots * a.H);
-    if (item < 0) return;
-    const int h = (int)(item / slots);
+    int h;
+    int64_t slot;
+    head_and_slot(slots, a.H, h, slot);
     int n, q0, Lq, Lk;
     int64_t qs, ks;
-    if (!tile_of(a.cuq, a.N, a.Tq, BM, slots - 1 - item % slots, lane, n, qs, Lq, q0)) return;
+    if (!tile_of(a.cuq, a.N, a.Tq, BM, slots - 1 - slot, lane, n, qs, Lq, q0)) return;
     const bool rest = a.cuq && n == a.N;
     if (rest && !a.zero_rest) return;
     seq_range(a.cuk, a.N, rest ? 0 : n, a.Tk, ks, Lk);
@@ -180,7 +180,7 @@ template <class T> __global__ __launch_bounds__(256) void mla_dkr_kernel(MlaArgs
 template <class T, int DN, int DR> hipError_t launch_dq(const MlaArgs& a, hipStream_t s) {
     if (a.Tq == 0) return hipSuccess;
     const int64_t slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 128), items = slots * a.H;
-    mla_dq_kernel<T, DN, DR><<<dim3((unsigned)((items + 7) / 8 * 8)), 256, 0, s>>>(a, slots);
+    mla_dq_kernel<T, DN, DR><<<dim3((unsigned)items), 256, 0, s>>>(a, slots);
     return hipGetLastError();
 }
 template <class T> hipError_t launch_dq_dims(const MlaArgs& a, hipStream_t s) {

@@ -295,13 +295,20 @@ __device__ __forceinline__ void wait_loads_and_lds() {
     asm volatile("" ::: "memory");
 }
 
-// Blocks are dealt round-robin over the 8 XCDs, each with an L2 of its own:
-// this gives XCD x the x-th contiguous eighth of a list of n items, so that
-// the items that share data (a head's tiles) share an L2. Returns -1 past the
-// end. The grid is 8 * ceil(n / 8) blocks.
-__device__ __forceinline__ int64_t xcd_item(int64_t n) {
-    const int64_t per = (n + 7) / 8, i = (int64_t)(blockIdx.x & 7) * per + (blockIdx.x >> 3);
-    return (int64_t)(blockIdx.x >> 3) < per && i < n ? i : -1;
+// Which head and which slot of the tile list a workgroup takes. Workgroups are
+// dealt round-robin over the 8 XCDs, each with an L2 of its own, and start in
+// the order of their index. Heads go fastest, so that with a multiple of 8 of
+// them every head stays on one XCD, where its tiles share the L2; slots go by
+// falling work, so that no long tile starts last (heads one after the other,
+// each from its longest tile, left a fifth of the wave slots empty at 4096
+// tokens); and 32 heads go at a time, 4 on an XCD, so that enough of a head's
+// tiles walk through the same keys together.
+__device__ __forceinline__ void head_and_slot(int64_t slots, int H, int& h, int64_t& slot) {
+    const int64_t item = blockIdx.x;
+    const int g = (int)(item / (32 * slots)) * 32, n = H - g < 32 ? H - g : 32;
+    const int64_t r = item - g * slots;
+    h = g + (int)(r % n);
+    slot = r / n;
 }
 
 // Start and length of sequence n (dense: rows of T; packed: offsets cu,

@@ -21,12 +21,12 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
     __shared__ __attribute__((aligned(16))) float stat[2][2][BQ];     // lse (base 2) and D of the tile's rows
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n32 = lane & 31, hf = lane >> 5;
-    const int64_t item = xcd_item(slots * a.H);
-    if (item < 0) return;
-    const int h = (int)(item / slots);
+    int h;
+    int64_t slot;
+    head_and_slot(slots, a.H, h, slot);
     int n, k0, Lq, Lk;
     int64_t qs, ks;
-    if (!tile_of(a.cuk, a.N, a.Tk, BK, item % slots, lane, n, ks, Lk, k0)) return;
+    if (!tile_of(a.cuk, a.N, a.Tk, BK, slot, lane, n, ks, Lk, k0)) return;
     const bool rest = a.cuk && n == a.N;
     if (rest && !a.zero_rest) return;
     seq_range(a.cuq, a.N, rest ? 0 : n, a.Tq, qs, Lq);
@@ -174,7 +174,7 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
 template <class T, int DN, int DR> hipError_t launch_dkv(const MlaArgs& a, hipStream_t s) {
     if (a.Tk == 0) return hipSuccess;
     const int64_t slots = tile_slots(a.cuk, a.B, a.N, a.Tk, 128), items = slots * a.H;
-    mla_dkv_kernel<T, DN, DR><<<dim3((unsigned)((items + 7) / 8 * 8)), 256, 0, s>>>(a, slots);
+    mla_dkv_kernel<T, DN, DR><<<dim3((unsigned)items), 256, 0, s>>>(a, slots);
     return hipGetLastError();
 }
 template <class T> hipError_t launch_dkv_dims(const MlaArgs& a, hipStream_t s) {

@@ -28,10 +28,10 @@ __global__ __launch_bounds__(256, QB == 1 && sizeof(T) == 2 ? 2 : 1) void mla_fw
     __shared__ __attribute__((aligned(1024))) char smem[2][kBuf];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n32 = lane & 31, hf = lane >> 5;
-    const int64_t item = xcd_item(slots * a.H);
-    if (item < 0) return;
-    const int h = (int)(item / slots);
-    const int64_t slot = slots - 1 - item % slots;      // a sequence's longest rows of keys first
+    int h;
+    int64_t slot;
+    head_and_slot(slots, a.H, h, slot);
+    slot = slots - 1 - slot;                            // a sequence's longest rows of keys first
     int n, q0, Lq, Lk;
     int64_t qs, ks;
     if (!tile_of(a.cuq, a.N, a.Tq, BM, slot, lane, n, qs, Lq, q0)) return;
@@ -218,7 +218,7 @@ template <class T, int DN, int DR, int QB> hipError_t launch(const MlaArgs& a, h
     const int64_t slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 128 * QB);
     const int64_t items = slots * a.H;
     if (items == 0) return hipSuccess;
-    mla_fwd_kernel<T, DN, DR, QB><<<dim3((unsigned)((items + 7) / 8 * 8)), 256, 0, s>>>(a, slots);
+    mla_fwd_kernel<T, DN, DR, QB><<<dim3((unsigned)items), 256, 0, s>>>(a, slots);
     return hipGetLastError();
 }
 

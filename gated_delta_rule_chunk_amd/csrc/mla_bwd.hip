@@ -105,14 +105,19 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
         for (int kb = 0; kb < KB; ++kb) {
             const int k0 = t * BN + 32 * kb;
             if (a.causal && k0 > wq0 + 31 + off) continue;
+            // LDS addresses are formed anew for each block: kept over the
+            // loop, they push operands out of the registers
+            int ln = lane;
+            asm volatile("" : "+v"(ln));
+            const int ln32 = ln & 31, lhf = ln >> 5;
             f32x16 sc = zero16(), dp = zero16();
 #pragma unroll
             for (int s = 0; s < DQ / 16; ++s) {
                 if (s < DN / 16) {
-                    sc = mma(read_rows<T, CK>(buf, 32 * kb + n32, s, hf), qf[s], sc);
-                    dp = mma(read_rows<T, CK>(buf + kK, 32 * kb + n32, s, hf), df[s < DN / 16 ? s : 0], dp);
+                    sc = mma(read_rows<T, CK>(buf, 32 * kb + ln32, s, lhf), qf[s], sc);
+                    dp = mma(read_rows<T, CK>(buf + kK, 32 * kb + ln32, s, lhf), df[s < DN / 16 ? s : 0], dp);
                 } else if constexpr (DR > 0) {
-                    sc = mma(read_rows<T, CR>(buf + 2 * kK, 32 * kb + n32, s - DN / 16, hf), qf[s], sc);
+                    sc = mma(read_rows<T, CR>(buf + 2 * kK, 32 * kb + ln32, s - DN / 16, lhf), qf[s], sc);
                 }
             }
             if constexpr (sizeof(T) == 2) sched_reads_under_mma<6, 1, (DQ + DN) / 16 - 6>();
@@ -129,10 +134,10 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
             auto read = [&](int i) -> Frag<T> {
                 const int s = i / (DQ / 32), d = i % (DQ / 32);
                 if constexpr (DR > 0)
-                    if (d >= DN / 32) return read_cols<T, CR>(buf + 2 * kK, 32 * kb + 16 * s, 32 * d - DN, lane);
-                return read_cols<T, CK>(buf, 32 * kb + 16 * s, 32 * d, lane);
+                    if (d >= DN / 32) return read_cols<T, CR>(buf + 2 * kK, 32 * kb + 16 * s, 32 * d - DN, ln);
+                return read_cols<T, CK>(buf, 32 * kb + 16 * s, 32 * d, ln);
             };
-            ReadAhead<T, DQ / 16, 2> ahead;
+            ReadAhead<T, DQ / 16, 3> ahead;
             ahead.start(read);
 #pragma unroll
             for (int r = 0; r < 16; ++r) {

@@ -22,16 +22,16 @@ namespace {
 
 using namespace mla;
 
-template <class T> constexpr int kBwdKeys = sizeof(T) == 2 ? 64 : 32;     // keys a tile (dq)
-
-template <class T, int DN, int DR>
-__global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(MlaArgs a, int64_t slots) {
-    constexpr int DQ = DN + DR, BN = kBwdKeys<T>, KB = BN / 32, BM = 128;
+template <class T, int DN, int DR, bool SPLIT>
+__global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_kernel(MlaArgs a, int64_t slots) {
+    constexpr int DQ = DN + DR, BN = sizeof(T) == 2 && !SPLIT ? 64 : 32, KB = BN / 32, BM = SPLIT ? 32 : 128;
     constexpr int CK = DN / kChunk<T>, CR = DR / kChunk<T>;
-    constexpr int kK = BN * CK * 16, kR = BN * CR * 16, kBuf = 2 * kK + kR;
-    __shared__ __attribute__((aligned(1024))) char smem[2][kBuf];
+    constexpr int kK = BN * CK * 16, kR = BN * CR * 16, kTileBytes = 2 * kK + kR;
+    constexpr int kBuf = SPLIT ? larger(kTileBytes, DQ * 128) : kTileBytes;    // split: also the exchange
+    constexpr int kLoaders = SPLIT ? 1 : 4;
+    __shared__ __attribute__((aligned(1024))) char smem[SPLIT ? 4 : 2][kBuf];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n32 = lane & 31, hf = lane >> 5;
+    const int n32 = lane & 31, hf = lane >> 5, lw = SPLIT ? 0 : w;
     int h;
     int64_t slot;
     head_and_slot(slots, a.H, h, slot);
@@ -43,7 +43,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
     seq_range(a.cuk, a.N, rest ? 0 : n, a.Tk, ks, Lk);
     if (rest) Lk = 0;
     const int off = Lk - Lq;
-    const int wq0 = q0 + 32 * w;
+    const int wq0 = q0 + 32 * lw;
     const int last = (q0 + BM < Lq ? q0 + BM : Lq) - 1;
     int keys = Lk;
     if (a.causal) keys = last + off + 1 < Lk ? last + off + 1 : Lk;
@@ -76,7 +76,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
             for (int j = 0; j < 8; ++j) delta += (float)df[s][j] * (float)of[j];
         }
         delta = half_sum(delta);
-        if (live && hf == 0 && !rest) a.delta[srow] = delta;
+        if (live && hf == 0 && !rest && w == (SPLIT ? 0 : w)) a.delta[srow] = delta;
     }
     f32x16 acc[DQ / 32];
 #pragma unroll
@@ -85,22 +85,17 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
     // a row without a visible key has lse -inf; all its terms are hidden below
     const float lse = rest ? 0.f : a.lse[srow], l2 = lse == -INFINITY ? 0.f : lse * kLog2e;
 
-    TileLoad<CK, BN, 4> lk;
-    TileLoad<DR ? CR : 8, BN, 4> lr;
-    lk.init(kvs, w, lane);
-    if constexpr (DR > 0) lr.init(krs, w, lane);
+    TileLoad<CK, BN, kLoaders> lk;
+    TileLoad<DR ? CR : 8, BN, kLoaders> lr;
+    lk.init(kvs, lw, lane);
+    if constexpr (DR > 0) lr.init(krs, lw, lane);
     auto load = [&](int t, char* buf) {
         const int k0 = t * BN, rmax = Lk - 1 - k0;
-        lk.load(buf, kvp + k0 * kvs, kvs, rmax, w, lane);
-        lk.load(buf + kK, kvp + DN * sizeof(T) + k0 * kvs, kvs, rmax, w, lane);
-        if constexpr (DR > 0) lr.load(buf + 2 * kK, krp + k0 * krs, krs, rmax, w, lane);
+        lk.load(buf, kvp + k0 * kvs, kvs, rmax, lw, lane);
+        lk.load(buf + kK, kvp + DN * sizeof(T) + k0 * kvs, kvs, rmax, lw, lane);
+        if constexpr (DR > 0) lr.load(buf + 2 * kK, krp + k0 * krs, krs, rmax, lw, lane);
     };
-    if (tiles > 0) load(0, smem[0]);
-    wait_loads_and_lds();
-    wg_barrier();
-    for (int t = 0; t < tiles; ++t) {
-        const char* buf = smem[t & 1];
-        if (t + 1 < tiles) load(t + 1, smem[(t + 1) & 1]);
+    auto compute = [&](int t, const char* buf) {
 #pragma unroll
         for (int kb = 0; kb < KB; ++kb) {
             const int k0 = t * BN + 32 * kb;
@@ -145,16 +140,39 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_dq_kernel(Mla
                 sc[r] = p * (dp[r] - delta);
             }
             const Frag<T> f[2] = {to_frag<T>(sc, 0), to_frag<T>(sc, 1)};
-            ahead.template run<1>(read, [&](int i, const Frag<T>& x) {
+            ahead.run(read, [&](int i, const Frag<T>& x) {
                 acc[i % (DQ / 32)] = mma(x, f[i / (DQ / 32)], acc[i % (DQ / 32)]);
             });
         }
+    };
+    T* p = static_cast<T*>(a.dq) + qrow * DQ;
+    if constexpr (SPLIT) {
+        for (int t = w; t < tiles; t += 4) {
+            load(t, smem[w]);
+            wait_loads_and_lds();
+            compute(t, smem[w]);
+            wait_loads_and_lds();
+        }
+#pragma unroll
+        for (int d = 0; d < DQ / 32; ++d) put_block(smem[w], d, acc[d], lane);
         wait_loads_and_lds();
         wg_barrier();
-    }
-    T* p = static_cast<T*>(a.dq) + qrow * DQ;
+        const float one[4] = {1.f, 1.f, 1.f, 1.f};
+        for (int d = w; d < DQ / 32; d += 4)
+            store_tile<T>(p + 32 * d, sum_blocks(smem[0], kBuf, d, one, lane), a.scale, hf, live);
+    } else {
+        if (tiles > 0) load(0, smem[0]);
+        wait_loads_and_lds();
+        wg_barrier();
+        for (int t = 0; t < tiles; ++t) {
+            if (t + 1 < tiles) load(t + 1, smem[(t + 1) & 1]);
+            compute(t, smem[t & 1]);
+            wait_loads_and_lds();
+            wg_barrier();
+        }
 #pragma unroll
-    for (int d = 0; d < DQ / 32; ++d) store_tile<T>(p + 32 * d, acc[d], a.scale, hf, live);
+        for (int d = 0; d < DQ / 32; ++d) store_tile<T>(p + 32 * d, acc[d], a.scale, hf, live);
+    }
 }
 
 // Sums the shared key part's shares over the heads, in their order: four
@@ -184,8 +202,13 @@ template <class T> __global__ __launch_bounds__(256) void mla_dkr_kernel(MlaArgs
 
 template <class T, int DN, int DR> hipError_t launch_dq(const MlaArgs& a, hipStream_t s) {
     if (a.Tq == 0) return hipSuccess;
-    const int64_t slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 128), items = slots * a.H;
-    mla_dq_kernel<T, DN, DR><<<dim3((unsigned)items), 256, 0, s>>>(a, slots);
+    int64_t slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 128);
+    if (slots * a.H < kSmallLaunch) {
+        slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 32);
+        mla_dq_kernel<T, DN, DR, true><<<dim3((unsigned)(slots * a.H)), 256, 0, s>>>(a, slots);
+    } else {
+        mla_dq_kernel<T, DN, DR, false><<<dim3((unsigned)(slots * a.H)), 256, 0, s>>>(a, slots);
+    }
     return hipGetLastError();
 }
 template <class T> hipError_t launch_dq_dims(const MlaArgs& a, hipStream_t s) {

@@ -149,7 +149,7 @@ template <class T, int N, int AHEAD> struct ReadAhead {
         for (int i = 0; i < kAhead; ++i) ring[i] = read(i);
         __builtin_amdgcn_sched_barrier(0);
     }
-    template <int MMAS, class Read, class Use> __device__ __forceinline__ void run(Read read, Use use) {
+    template <class Read, class Use> __device__ __forceinline__ void run(Read read, Use use) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -159,7 +159,7 @@ template <class T, int N, int AHEAD> struct ReadAhead {
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int i = 0; i < N - kAhead; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, MMAS, 0);     // products with one operand
+                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);        // a product
                 __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);        // two transposing reads
             }
         }
@@ -280,6 +280,8 @@ __device__ __forceinline__ void store_tile(T* p, const f32x16& acc, float mul, i
     }
 }
 
+constexpr int larger(int a, int b) { return a > b ? a : b; }
+
 // The workgroup barrier without a fence: every wave has waited for its own
 // loads and LDS accesses before it (wait_loads_and_lds).
 __device__ __forceinline__ void wg_barrier() {
@@ -293,6 +295,33 @@ __device__ __forceinline__ void wait_loads_and_lds() {
     asm volatile("" ::: "memory");
     __builtin_amdgcn_s_waitcnt(0x0070);   // vmcnt(0), lgkmcnt(0)
     asm volatile("" ::: "memory");
+}
+
+// Split kernels: where a launch would leave compute units idle, the four waves
+// of a workgroup take the same 32 rows and every fourth tile of the other side
+// each, with a tile buffer of their own, and their sums meet in LDS at the end.
+// A launch counts as small below one workgroup per compute unit.
+constexpr int64_t kSmallLaunch = 256;
+
+// A wave's accumulator block d to and from its exchange region
+__device__ __forceinline__ void put_block(char* region, int d, const f32x16& x, int lane) {
+#pragma unroll
+    for (int g = 0; g < 4; ++g)
+        *reinterpret_cast<f32x4*>(region + ((d * 4 + g) * 64 + lane) * 16) =
+            f32x4{x[4 * g], x[4 * g + 1], x[4 * g + 2], x[4 * g + 3]};
+}
+// block d of the four regions, `stride` bytes apart, each times its factor
+__device__ __forceinline__ f32x16 sum_blocks(const char* regions, int stride, int d, const float (&f)[4], int lane) {
+    f32x16 s = zero16();
+#pragma unroll
+    for (int v = 0; v < 4; ++v)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+            const f32x4 x = *reinterpret_cast<const f32x4*>(regions + v * stride + ((d * 4 + g) * 64 + lane) * 16);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[4 * g + j] += f[v] * x[j];
+        }
+    return s;
 }
 
 // Which head and which slot of the tile list a workgroup takes. Workgroups are

@@ -10,17 +10,18 @@
 namespace kda {
 namespace mla {
 
-template <class T> constexpr int kBwdRows = sizeof(T) == 2 ? 64 : 32;     // queries a tile
-
-template <class T, int DN, int DR>
+template <class T, int DN, int DR, bool SPLIT>
 __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slots) {
-    constexpr int DQ = DN + DR, BQ = kBwdRows<T>, QB = BQ / 32, BK = 128;
-    constexpr int CN = DN / kChunk<T>, CR = DR / kChunk<T>;
-    constexpr int kQ = BQ * CN * 16, kBuf = 2 * kQ + BQ * CR * 16;    // q's own part, d_o, q's shared part
-    __shared__ __attribute__((aligned(1024))) char smem[2][kBuf];
-    __shared__ __attribute__((aligned(16))) float stat[2][2][BQ];     // lse (base 2) and D of the tile's rows
+    constexpr int DQ = DN + DR, BQ = sizeof(T) == 2 && !SPLIT ? 64 : 32, QB = BQ / 32, BK = SPLIT ? 32 : 128;
+    constexpr int CN = DN / kChunk<T>, CR = DR / kChunk<T>, NV = DN / 32, NK = DQ / 32;
+    constexpr int kQ = BQ * CN * 16, kTileBytes = 2 * kQ + BQ * CR * 16;       // q's own part, d_o, q's shared part
+    constexpr int kBuf = SPLIT ? larger(kTileBytes, (NV + NK) * 4096) : kTileBytes;    // split: also the exchange
+    constexpr int kLoaders = SPLIT ? 1 : 4;
+    __shared__ __attribute__((aligned(1024))) char smem[SPLIT ? 4 : 2][kBuf];
+    // lse (base 2) and D of the tile's rows; split: in registers, row n32 on lane n32
+    __shared__ __attribute__((aligned(16))) float stat[SPLIT ? 1 : 2][2][SPLIT ? 1 : BQ];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n32 = lane & 31, hf = lane >> 5;
+    const int n32 = lane & 31, hf = lane >> 5, lw = SPLIT ? 0 : w;
     int h;
     int64_t slot;
     head_and_slot(slots, a.H, h, slot);
@@ -32,7 +33,7 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
     seq_range(a.cuq, a.N, rest ? 0 : n, a.Tq, qs, Lq);
     if (rest) Lq = 0;
     const int off = Lk - Lq;
-    const int wk0 = k0 + 32 * w, j = wk0 + n32, jc = j < Lk ? j : Lk - 1;
+    const int wk0 = k0 + 32 * lw, j = wk0 + n32, jc = j < Lk ? j : Lk - 1;
     // the first query that sees the block's first key, down to a tile's start
     int first = 0;
     if (a.causal && k0 - off > 0) first = (k0 - off) / BQ * BQ;
@@ -65,45 +66,26 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
     const char* dp_ = static_cast<const char*>(a.d_o) + (qs * a.H + h) * DN * (int64_t)sizeof(T);
     const int64_t srow = ((a.cuq ? 0 : (int64_t)n * a.H) + h) * a.Tq + (a.cuq ? qs : 0);
 
-    TileLoad<CN, BQ, 4> lq, ld;
-    TileLoad<DR ? CR : 8, BQ, 4> lr;
-    lq.init(qst, w, lane);
-    ld.init(ost, w, lane);
-    if constexpr (DR > 0) lr.init(qst, w, lane);
+    TileLoad<CN, BQ, kLoaders> lq, ld;
+    TileLoad<DR ? CR : 8, BQ, kLoaders> lr;
+    lq.init(qst, lw, lane);
+    ld.init(ost, lw, lane);
+    if constexpr (DR > 0) lr.init(qst, lw, lane);
     auto load = [&](int t, char* buf) {
         const int r0 = first + t * BQ, rmax = Lq - 1 - r0;
-        lq.load(buf, qp + r0 * qst, qst, rmax, w, lane);
-        ld.load(buf + kQ, dp_ + r0 * ost, ost, rmax, w, lane);
-        if constexpr (DR > 0) lr.load(buf + 2 * kQ, qp + DN * sizeof(T) + r0 * qst, qst, rmax, w, lane);
+        lq.load(buf, qp + r0 * qst, qst, rmax, lw, lane);
+        ld.load(buf + kQ, dp_ + r0 * ost, ost, rmax, lw, lane);
+        if constexpr (DR > 0) lr.load(buf + 2 * kQ, qp + DN * sizeof(T) + r0 * qst, qst, rmax, lw, lane);
     };
     // Rows past the sequence and rows without a visible key get lse = +inf,
     // which makes all their terms zero.
-    auto load_stat = [&](int t, float& x) {
-        const int r = first + t * BQ + (threadIdx.x & (BQ - 1));
-        if ((int)threadIdx.x < BQ) {
-            x = r < Lq ? a.lse[srow + r] * kLog2e : INFINITY;
-            if (x == -INFINITY) x = INFINITY;
-        } else if ((int)threadIdx.x < 2 * BQ) {
-            x = r < Lq ? a.delta[srow + r] : 0.f;
-        }
+    auto row_lse = [&](int r) {
+        const float x = r < Lq ? a.lse[srow + r] * kLog2e : INFINITY;
+        return x == -INFINITY ? INFINITY : x;
     };
-    auto put_stat = [&](int b, float x) {
-        if ((int)threadIdx.x < 2 * BQ) stat[b][threadIdx.x / BQ][threadIdx.x % BQ] = x;
-    };
-    float x = 0.f;
-    if (tiles > 0) {
-        load(0, smem[0]);
-        load_stat(0, x);
-        put_stat(0, x);
-    }
-    wait_loads_and_lds();
-    wg_barrier();
-    for (int t = 0; t < tiles; ++t) {
-        const char* buf = smem[t & 1];
-        if (t + 1 < tiles) {
-            load_stat(t + 1, x);
-            load(t + 1, smem[(t + 1) & 1]);
-        }
+    auto row_delta = [&](int r) { return r < Lq ? a.delta[srow + r] : 0.f; };
+    // stats(qb, g, l2, de): lse and D of rows 8 g + 4 hf .. + 3 of query block qb
+    auto compute = [&](int t, const char* buf, auto stats) {
 #pragma unroll
         for (int qb = 0; qb < QB; ++qb) {
             const int r0 = first + t * BQ + 32 * qb;       // query r0 sees keys <= r0 + off
@@ -124,7 +106,7 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
 #pragma unroll
                 for (int r = 0; r < 16; ++r) sc[r] = 8 * (r / 4) + r % 4 < lim ? -INFINITY : sc[r];
             }
-            constexpr int NV = DN / 32, NK = DQ / 32;       // operands of a step: d_o for dv, then q for dk
+            // operands of a step: d_o for dv, then q for dk
             auto read = [&](int i) -> Frag<T> {
                 const int s = i / (NV + NK), d = i % (NV + NK);
                 if (d < NV) return read_cols<T, CN>(buf + kQ, 32 * qb + 16 * s, 32 * d, lane);
@@ -136,8 +118,8 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
             ahead.start(read);
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const f32x4 l2 = *reinterpret_cast<const f32x4*>(&stat[t & 1][0][32 * qb + 8 * g + 4 * hf]);
-                const f32x4 de = *reinterpret_cast<const f32x4*>(&stat[t & 1][1][32 * qb + 8 * g + 4 * hf]);
+                f32x4 l2, de;
+                stats(qb, g, l2, de);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const int r = 4 * g + e;
@@ -147,34 +129,89 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
             }
             const Frag<T> pf[2] = {to_frag<T>(sc, 0), to_frag<T>(sc, 1)};
             const Frag<T> sf[2] = {to_frag<T>(dp, 0), to_frag<T>(dp, 1)};
-            ahead.template run<1>(read, [&](int i, const Frag<T>& x) {
+            ahead.run(read, [&](int i, const Frag<T>& x) {
                 const int s = i / (NV + NK), d = i % (NV + NK);
                 if (d < NV) dv[d] = mma(x, pf[s], dv[d]);
                 else dk[d - NV] = mma(x, sf[s], dk[d - NV]);
             });
         }
-        if (t + 1 < tiles) put_stat((t + 1) & 1, x);
-        wait_loads_and_lds();
-        wg_barrier();
-    }
+    };
     const bool live = j < Lk;
     T* p = static_cast<T*>(a.dkv) + kvrow * 2 * DN;
+    float* r = nullptr;
+    if constexpr (DR > 0) r = a.dkr_part + (((int64_t)h * a.B + (a.cuk ? 0 : n)) * a.Tk + (a.cuk ? ks + jc : jc)) * DR;
+    // block d of the results: dk, then dv
+    auto store = [&](int d, const f32x16& x) {
+        if (d < NV) store_tile<T>(p + 32 * d, x, a.scale, hf, live);
+        else if (d < NK) store_tile<float>(r + 32 * (d - NV), x, a.scale, hf, live);
+        else store_tile<T>(p + DN + 32 * (d - NK), x, 1.f, hf, live);
+    };
+    if constexpr (SPLIT) {
+        for (int t = w; t < tiles; t += 4) {
+            load(t, smem[w]);
+            const int row = first + t * BQ + n32;
+            const float ls = row_lse(row), dl = row_delta(row);
+            wait_loads_and_lds();
+            compute(t, smem[w], [&](int, int g, f32x4& l2, f32x4& de) {
 #pragma unroll
-    for (int d = 0; d < DN / 32; ++d) {
-        store_tile<T>(p + 32 * d, dk[d], a.scale, hf, live);
-        store_tile<T>(p + DN + 32 * d, dv[d], 1.f, hf, live);
-    }
-    if constexpr (DR > 0) {
-        float* r = a.dkr_part + (((int64_t)h * a.B + (a.cuk ? 0 : n)) * a.Tk + (a.cuk ? ks + jc : jc)) * DR;
+                for (int e = 0; e < 4; ++e) {
+                    l2[e] = __shfl(ls, 8 * g + 4 * hf + e);
+                    de[e] = __shfl(dl, 8 * g + 4 * hf + e);
+                }
+            });
+            wait_loads_and_lds();
+        }
 #pragma unroll
-        for (int d = 0; d < DR / 32; ++d) store_tile<float>(r + 32 * d, dk[DN / 32 + d], a.scale, hf, live);
+        for (int d = 0; d < NK; ++d) put_block(smem[w], d, dk[d], lane);
+#pragma unroll
+        for (int d = 0; d < NV; ++d) put_block(smem[w], NK + d, dv[d], lane);
+        wait_loads_and_lds();
+        wg_barrier();
+        const float one[4] = {1.f, 1.f, 1.f, 1.f};
+        for (int d = w; d < NK + NV; d += 4) store(d, sum_blocks(smem[0], kBuf, d, one, lane));
+    } else {
+        const int sr = threadIdx.x % BQ, sk = threadIdx.x / BQ;   // what this thread fetches of the statistics
+        auto fetch = [&](int t) -> float {
+            if (sk == 0) return row_lse(first + t * BQ + sr);
+            return sk == 1 ? row_delta(first + t * BQ + sr) : 0.f;
+        };
+        if (tiles > 0) {
+            load(0, smem[0]);
+            const float x = fetch(0);
+            if (sk < 2) stat[0][sk][sr] = x;
+        }
+        wait_loads_and_lds();
+        wg_barrier();
+        for (int t = 0; t < tiles; ++t) {
+            float x = 0.f;
+            if (t + 1 < tiles) {
+                x = fetch(t + 1);
+                load(t + 1, smem[(t + 1) & 1]);
+            }
+            compute(t, smem[t & 1], [&](int qb, int g, f32x4& l2, f32x4& de) {
+                l2 = *reinterpret_cast<const f32x4*>(&stat[t & 1][0][32 * qb + 8 * g + 4 * hf]);
+                de = *reinterpret_cast<const f32x4*>(&stat[t & 1][1][32 * qb + 8 * g + 4 * hf]);
+            });
+            if (t + 1 < tiles && sk < 2) stat[(t + 1) & 1][sk][sr] = x;
+            wait_loads_and_lds();
+            wg_barrier();
+        }
+#pragma unroll
+        for (int d = 0; d < NK; ++d) store(d, dk[d]);
+#pragma unroll
+        for (int d = 0; d < NV; ++d) store(NK + d, dv[d]);
     }
 }
 
 template <class T, int DN, int DR> hipError_t launch_dkv(const MlaArgs& a, hipStream_t s) {
     if (a.Tk == 0) return hipSuccess;
-    const int64_t slots = tile_slots(a.cuk, a.B, a.N, a.Tk, 128), items = slots * a.H;
-    mla_dkv_kernel<T, DN, DR><<<dim3((unsigned)items), 256, 0, s>>>(a, slots);
+    int64_t slots = tile_slots(a.cuk, a.B, a.N, a.Tk, 128);
+    if (slots * a.H < kSmallLaunch) {
+        slots = tile_slots(a.cuk, a.B, a.N, a.Tk, 32);
+        mla_dkv_kernel<T, DN, DR, true><<<dim3((unsigned)(slots * a.H)), 256, 0, s>>>(a, slots);
+    } else {
+        mla_dkv_kernel<T, DN, DR, false><<<dim3((unsigned)(slots * a.H)), 256, 0, s>>>(a, slots);
+    }
     return hipGetLastError();
 }
 template <class T> hipError_t launch_dkv_dims(const MlaArgs& a, hipStream_t s) {

@@ -65,6 +65,17 @@ def test_packed_ragged(dtype, H, Dn, Dr):
     _both(q, kv, kr, d_o, cuq, cuk, lens, False, scale=0.3)
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Dn,Dr", DIMS)
+def test_many_heads(dtype, Dn, Dr):
+    """Enough workgroups that the tiles are shared by a workgroup's waves (the
+    tests of few heads run the split kernels)."""
+    lens = [(130, 257), (100, 60), (1, 1), (64, 64), (0, 3)]
+    q, kv, kr, d_o, cuq, cuk = _make(lens, 61, Dn, Dr, dtype, 15, tail=3, grad=True)
+    _both(q, kv, kr, d_o, cuq, cuk, lens, True)
+    _both(q, kv, kr, d_o, cuq, cuk, lens, False)
+
+
 def test_many_short_sequences():
     """More sequences than a wave's lanes: the tile search takes several steps."""
     lens = [(i % 5, i % 5 + i % 3) for i in range(200)]

@@ -251,6 +251,9 @@ kda_status kda_mla_step(const void* q_latent, int64_t q_latent_n, int64_t q_late
     if (kda_status st = check_scale(fn, scale)) return st;
     if (!q_latent || (Dr == 0) != (q_rope == nullptr))
         return fail(KDA_ERR_INVALID_ARG, "%s: q_latent must be non-NULL, q_rope NULL if and only if Dr = 0", fn);
+    // the kernels count the cache's 32-row tiles in 31 bits
+    if ((int64_t)Nb * (((int64_t)max_pages * page_size + 31) / 32) > ((int64_t)1 << 30))
+        return fail(KDA_ERR_UNSUPPORTED, "%s: Nb * max_pages * page_size too large", fn);
     const int64_t st[] = {q_latent_n, q_latent_t, q_latent_h, q_rope_n, q_rope_t, q_rope_h};
     for (int i = 0; i < (Dr ? 6 : 3); ++i)
         if (!stride_ok(st[i], dtype))

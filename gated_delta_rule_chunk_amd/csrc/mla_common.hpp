@@ -149,7 +149,8 @@ template <class T, int N, int AHEAD> struct ReadAhead {
         for (int i = 0; i < kAhead; ++i) ring[i] = read(i);
         __builtin_amdgcn_sched_barrier(0);
     }
-    template <class Read, class Use> __device__ __forceinline__ void run(Read read, Use use) {
+    // MMAS products with each operand of READS LDS reads
+    template <int MMAS = 1, int READS = 2, class Read, class Use> __device__ __forceinline__ void run(Read read, Use use) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -159,8 +160,8 @@ template <class T, int N, int AHEAD> struct ReadAhead {
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int i = 0; i < N - kAhead; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);        // a product
-                __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);        // two transposing reads
+                __builtin_amdgcn_sched_group_barrier(0x008, MMAS, 0);
+                __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
@@ -278,6 +279,18 @@ __device__ __forceinline__ void store_tile(T* p, const f32x16& acc, float mul, i
             }
         }
     }
+}
+
+__device__ __forceinline__ void wait_lds() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0)
+    asm volatile("" ::: "memory");
+}
+// ... but for the last N loads issued (vmcnt(N), lgkmcnt(0))
+template <int N> __device__ __forceinline__ void wait_all_but() {
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt((N & 15) | (N >> 4) << 14 | 0x0070);
+    asm volatile("" ::: "memory");
 }
 
 constexpr int larger(int a, int b) { return a > b ? a : b; }

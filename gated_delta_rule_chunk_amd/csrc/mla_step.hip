@@ -5,14 +5,17 @@
 // The rows of queries (token, head) of one sequence all read the same cache
 // rows, so a workgroup takes up to 128 of them and a run of the cache, and
 // every cache row is read from HBM once per 128 rows of queries. The cache goes
-// from global memory to LDS in tiles of 32 rows, two buffers. Two waves share
-// a block of 32 rows of queries: each forms the scores over half of the
-// columns (its half of the queries stays in registers) and, after they have
-// exchanged these sums through LDS, the output of half of the Dc columns, so
-// that its accumulators (Dc / 4 registers) leave room for two waves per SIMD.
+// from global memory to LDS in tiles, the next one under way while one is at
+// work.
+// Two waves share a block of 32 rows of queries: each forms the scores and
+// probabilities of 16 of them, and, after they have exchanged these (1 or 2 KB)
+// through LDS, the outputs of all 32 over half of the Dc columns. So a value
+// operand read from LDS, the costliest access here (it is read transposed),
+// serves two products, nothing is computed twice, and queries, scores and
+// outputs (Dc / 4 registers) leave room for two waves per SIMD.
 //
 // The work is split over the cache by its true lengths, which only the device
-// knows: the 32-row tiles of all sequences form one list, cut into equal
+// knows: the tiles of all sequences form one list, cut into equal
 // parts, one per workgroup. A workgroup walks through the sequences of its
 // part; a sequence that lies in one part is finished there, one that spans
 // several leaves (maximum, sum, output) of each part in the workspace, and a
@@ -28,33 +31,98 @@ namespace {
 using namespace mla;
 
 constexpr int kTile = 32;       // cache rows a tile
-// blocks of 32 rows of queries a workgroup, at most: what LDS holds
-template <class T, int DC> constexpr int max_blocks() { return sizeof(T) == 4 && DC == 512 ? 2 : 4; }
+// waves of 16 rows of queries a workgroup, at most (float32: what LDS holds)
+template <class T, int DC> constexpr int max_waves() { return sizeof(T) == 4 && DC == 512 ? 6 : 8; }
 
-// The list of tiles: rows of the cache that sequence b has
-__device__ __forceinline__ int row_len(const MlaStepArgs& a, int b) {
-    const int cap = a.max_pages << a.page_shift, n = a.lens[b];
-    return n < 0 ? 0 : n > cap ? cap : n;
+// Layout of a step of 32 products on 16x16 tiles (mla_common.hpp has the 32x32
+// ones): lane l with n = l % 16, g = l / 16 holds A row n and B column n,
+// products 8 g .. 8 g + 7, and accumulator register r is row 4 g + r, column
+// n. Two blocks of scores (keys 0-15, 16-31) make, as they stand, the B
+// operand over 32 keys whose product j of group g is key 4 g + j (j < 4) or 16
+// + 4 g + j - 4.
+__device__ __forceinline__ f32x4 mma16(bf16x8 a, bf16x8 b, f32x4 c) {
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(a, b, c, 0, 0, 0);
+}
+__device__ __forceinline__ f32x4 mma16(f32x8 a, f32x8 b, f32x4 c) {
+#pragma unroll
+    for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
+    return c;
+}
+// A operand over the columns: tile row r, columns 32 step + 8 g .. + 7
+template <class T, int RC> __device__ __forceinline__ Frag<T> read_rows16(const char* lds, int r, int step, int g) {
+    const char* p = lds + r * (RC * 16);
+    const int sw = swizzle<RC>(r);
+    if constexpr (sizeof(T) == 2) {
+        return *reinterpret_cast<const bf16x8*>(p + chunk_at<RC>(4 * step, g, sw));
+    } else {
+        const f32x4 a = *reinterpret_cast<const f32x4*>(p + chunk_at<RC>(8 * step, 2 * g, sw));
+        const f32x4 b = *reinterpret_cast<const f32x4*>(p + chunk_at<RC>(8 * step, 2 * g + 1, sw));
+        return f32x8{a[0], a[1], a[2], a[3], b[0], b[1], b[2], b[3]};
+    }
+}
+// A operand over 32 rows of a tile in the order above: row n = column col0 + n
+template <class T, int RC> __device__ __forceinline__ Frag<T> read_cols16(const char* lds, int col0, int lane) {
+    const int g = lane >> 4;
+    if constexpr (sizeof(T) == 2) {
+        bf16x8 f;
+#pragma unroll
+        for (int u = 0; u < 2; ++u) {
+            const int r = 16 * u + 4 * g + ((lane >> 2) & 3);
+            const char* p = lds + r * (RC * 16) + (lane & 1) * 8 + chunk_at<RC>(col0 >> 3, (lane & 3) >> 1, swizzle<RC>(r));
+            const bf16x4 b = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((KDA_LDS s16x4*)p));
+#pragma unroll
+            for (int j = 0; j < 4; ++j) f[4 * u + j] = b[j];
+        }
+        return f;
+    } else {
+        f32x8 f;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const int r = 16 * (j >> 2) + 4 * g + (j & 3);
+            f[j] = *reinterpret_cast<const float*>(lds + r * (RC * 16) + (lane & 3) * 4 +
+                                                   chunk_at<RC>(col0 >> 2, (lane & 15) >> 2, swizzle<RC>(r)));
+        }
+        return f;
+    }
+}
+// over the four lanes of a query row
+__device__ __forceinline__ float group_max(float v) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return half_max(fmaxf(__uint_as_float(p[0]), __uint_as_float(p[1])));
+}
+__device__ __forceinline__ float group_sum(float v) {
+    const auto p = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    return half_sum(__uint_as_float(p[0]) + __uint_as_float(p[1]));
+}
+// four consecutive columns
+__device__ __forceinline__ void store4(__bf16* p, const f32x4& x, float mul) {
+    *reinterpret_cast<uint2*>(p) = make_uint2(pack2_bf16(x[0] * mul, x[1] * mul), pack2_bf16(x[2] * mul, x[3] * mul));
+}
+__device__ __forceinline__ void store4(float* p, const f32x4& x, float mul) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{x[0] * mul, x[1] * mul, x[2] * mul, x[3] * mul};
 }
 
-// Inclusive sums of the tile counts of sequences b0 .. b0 + 63, one per lane.
-__device__ __forceinline__ int scan_tiles(const MlaStepArgs& a, int b0, int lane, int& cnt) {
-    cnt = b0 + lane < a.Nb ? (row_len(a, b0 + lane) + kTile - 1) / kTile : 0;
-    int sum = cnt;
+// The list of tiles, 64 sequences at a time, one per lane: rows of
+// the cache (cut to what the page table holds), tiles, and tiles up to and with
+// the sequence's.
+struct Scan {
+    int len, cnt, sum;
+    bool over;                  // the length says more than the table holds
+    __device__ __forceinline__ int all() const { return __builtin_amdgcn_readlane(sum, 63); }
+};
+__device__ __forceinline__ Scan scan_tiles(const MlaStepArgs& a, int b0, int lane) {
+    Scan x;
+    const int cap = a.max_pages << a.page_shift, n = b0 + lane < a.Nb ? a.lens[b0 + lane] : 0;
+    x.over = n > cap;
+    x.len = n < 0 ? 0 : x.over ? cap : n;
+    x.cnt = (x.len + kTile - 1) / kTile;
+    x.sum = x.cnt;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
-        const int v = __shfl_up(sum, d);
-        sum += lane >= d ? v : 0;
+        const int v = __shfl_up(x.sum, d);
+        x.sum += lane >= d ? v : 0;
     }
-    return sum;
-}
-__device__ __forceinline__ int all_tiles(const MlaStepArgs& a, int lane) {
-    int total = 0;
-    for (int b0 = 0; b0 < a.Nb; b0 += 64) {
-        int cnt;
-        total += __builtin_amdgcn_readlane(scan_tiles(a, b0, lane, cnt), 63);
-    }
-    return total;
+    return x;
 }
 // Tiles a part: an even share, but no fewer than keeps the partial results
 // (a part's cost of writing and joining them against the time of a tile).
@@ -68,60 +136,71 @@ __device__ __forceinline__ int part_tiles(const MlaStepArgs& a, int total) {
 // Partial result j (0: of a sequence begun in an earlier part, 1: of one that
 // goes on in the next) of a part and row of queries: maximum, sum, 2 unused, Dc values.
 __device__ __forceinline__ float* partial(const MlaStepArgs& a, int group, int part, int j, int row) {
-    return a.part + ((((int64_t)group * a.parts + part) * 2 + j) * (32 * a.blocks) + row) * (a.Dc + 4);
+    return a.part + ((((int64_t)group * a.parts + part) * 2 + j) * (16 * a.waves) + row) * (a.Dc + 4);
 }
 
-// A tile's 32 rows of RC chunks to LDS (layout: mla_common.hpp). Rows 0-15 lie
-// at lo and 16-31 at hi, 16 consecutive rows each. Lane l of instruction i
-// fills chunk 64 i + l of the tile; as a row's chunks are permuted within
-// their groups only, its source is that chunk with its low bits exchanged.
-// With EDGE, rows past rmax are not read (row rmax stands in), and halves
-// whose page does not exist (bits of have) are zeros: a hidden row's weight is
-// 0, but what it multiplies has to be finite.
+// A tile's rows of RC chunks to LDS (layout: mla_common.hpp), 16 consecutive
+// cache rows from each of two addresses. Lane l of a half's instruction j fills chunk 64 j + l of it; as a row's chunks are permuted within their
+// groups only, its source is that chunk with its low bits exchanged. With
+// EDGE, rows past rmax are not read (row rmax stands in), and halves whose
+// page does not exist (bits of have) are zeros: a hidden row's weight is 0, but
+// what it multiplies has to be finite.
 template <int RC, int WAVES, bool EDGE>
 __device__ __forceinline__ void load_cache_tile(char* lds, const char* lo, const char* hi, int rmax, int have, int w,
                                                 int lane) {
-    constexpr int kInstr = kTile * RC / 64, kHalf = kInstr / 2;
+    constexpr int kInstr = 16 * RC / 64;
     asm volatile("" : "+v"(lane));   // addresses are formed here for each tile, not kept in registers
 #pragma unroll
     for (int k = 0; k < (kInstr + WAVES - 1) / WAVES; ++k) {
-        const int i = k * WAVES + w;
-        if (kInstr % WAVES != 0 && i >= kInstr) break;
-        const int s = i * 64 + lane;
+        const int j = k * WAVES + w;
+        if (kInstr % WAVES != 0 && j >= kInstr) break;
+        const int s = j * 64 + lane;
         int r;
         if constexpr (RC % 64 == 0) {                     // an instruction stays in one row
-            r = i / (RC / 64);
+            r = j / (RC / 64);
         } else {                                          // a row has RC / 8 groups of 8 chunks
-            r = (int)((8u * (unsigned)i + ((unsigned)lane >> 3)) / (unsigned)(RC / 8));
+            r = (int)((8u * (unsigned)j + ((unsigned)lane >> 3)) / (unsigned)(RC / 8));
         }
         const int src = s ^ swizzle<RC>(r);
-        if constexpr (EDGE) {
-            const int half = i >= kHalf && rmax >= 16;    // where its rows come from
-            if (have >> half & 1) {
-                const int rr = r > rmax ? rmax : r;
-                load_lds16((rr < 16 ? lo : hi - 16 * RC * 16) + (src + (rr - r) * RC) * 16, lds + i * 1024);
+#pragma unroll
+        for (int q = 0; q < 2; ++q) {
+            char* to = lds + (q * kInstr + j) * 1024;
+            if constexpr (EDGE) {
+                const int f = 16 * q <= rmax ? q : 0;              // the half its rows come from
+                if (have >> f & 1) {
+                    const int last = rmax - 16 * f, rr = f < q || r > last ? last : r;
+                    load_lds16((f ? hi : lo) + (src + (rr - r) * RC) * 16, to);
+                } else {
+                    *reinterpret_cast<u32x4*>(to + lane * 16) = u32x4{0, 0, 0, 0};
+                }
             } else {
-                *reinterpret_cast<u32x4*>(lds + i * 1024 + lane * 16) = u32x4{0, 0, 0, 0};
+                load_lds16s(q ? hi : lo, src * 16, to);
             }
-        } else {
-            load_lds16s((i >= kHalf ? hi - 16 * RC * 16 : lo), src * 16, lds + i * 1024);
         }
     }
 }
 
-template <class T, int DC, int DR, int BLK>
-__global__ __launch_bounds__(128 * BLK, BLK > 2 ? 2 : 1) void mla_step_kernel(MlaStepArgs a) {
-    constexpr int D = DC + DR, RC = D / kChunk<T>, kBuf = kTile * RC * 16, WAVES = 2 * BLK;
-    constexpr int NS = D / 32, ND = DC / 64;          // this wave's steps of the scores, blocks of the output
-    // float32 queries do not fit the registers beside the output: they are
-    // read again for every tile (its products take 16 times as long as bf16's)
+template <class T, int DC, int DR, int WAVES>
+__global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel(MlaStepArgs a) {
+    constexpr int D = DC + DR, RC = D / kChunk<T>, kBuf = kTile * RC * 16;
+    constexpr int NS = D / 32, ND = DC / 32;          // steps of the scores, blocks of the output's half
+    // Not all queries fit the registers beside an output of 512 columns and what
+    // is under way: the first kLdsQ steps' of bf16 stay in LDS, and float32's
+    // are read again for every tile (its products take 16 times as long).
     constexpr bool kKeepQ = sizeof(T) == 2;
+    constexpr int kLdsQ = kKeepQ && DC == 512 ? 6 : 0;
     __shared__ __attribute__((aligned(1024))) char smem[2][kBuf];
-    __shared__ __attribute__((aligned(16))) float part_sc[WAVES][4][64][4];     // the waves' scores over their columns
-    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int n32 = lane & 31, hf = lane >> 5, half = w & 1;
+    // what the two waves of a row block tell each other: probabilities as
+    // operands, the factor of the running maximum's move (later 1 / sum)
+    __shared__ __attribute__((aligned(32))) Frag<T> probs[WAVES][64];
+    __shared__ float factor[WAVES][16];
+    __shared__ __attribute__((aligned(16))) Frag<T> lds_q[kLdsQ ? WAVES : 1][kLdsQ ? kLdsQ : 1][kLdsQ ? 64 : 1];
+    const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = w & 1;
     const int group = blockIdx.x % a.groups, part = blockIdx.x / a.groups;
-    const int total = all_tiles(a, lane), per = part_tiles(a, total);
+    Scan sq = scan_tiles(a, 0, lane);
+    int total = sq.all();
+    for (int b = 64; b < a.Nb; b += 64) total += scan_tiles(a, b, lane).all();
+    const int per = part_tiles(a, total);
     int at = part * per;                                         // next tile of the list
     const int end = total - at < per ? total : at + per;
     if (at >= total) return;
@@ -129,40 +208,37 @@ __global__ __launch_bounds__(128 * BLK, BLK > 2 ? 2 : 1) void mla_step_kernel(Ml
     const float c = a.scale * kLog2e;
     const int ps = a.page_shift;
 
-    int b0 = 0, cnt, sum = scan_tiles(a, 0, lane, cnt);
-    int before = 0;                                              // tiles of the sequences before b0
+    int b0 = 0, before = 0;                                      // sq's first sequence, tiles before it
     while (at < end) {
-        while (at >= before + __builtin_amdgcn_readlane(sum, 63)) {
-            before += __builtin_amdgcn_readlane(sum, 63);
+        while (at >= before + sq.all()) {
+            before += sq.all();
             b0 += 64;
-            sum = scan_tiles(a, b0, lane, cnt);
+            sq = scan_tiles(a, b0, lane);
         }
-        const int l = __ffsll((unsigned long long)__ballot(before + sum > at)) - 1;
+        const int l = __ffsll((unsigned long long)__ballot(before + sq.sum > at)) - 1;
         const int b = b0 + l;
-        const int tiles = __builtin_amdgcn_readlane(cnt, l);
-        const int first = before + __builtin_amdgcn_readlane(sum, l) - tiles;       // the sequence's place in the list
+        const int tiles = __builtin_amdgcn_readlane(sq.cnt, l), len = __builtin_amdgcn_readlane(sq.len, l);
+        const int first = before + __builtin_amdgcn_readlane(sq.sum, l) - tiles;    // the sequence's place in the list
         const int t0 = at - first, t1 = end - first < tiles ? end - first : tiles;
         at = first + t1;
-        const int len = __builtin_amdgcn_readfirstlane(row_len(a, b));
-        if (t0 == 0 && w == 0 && lane == 0 && group == 0 && a.lens[b] > len) atomicAdd(a.status, 1u);
+        if (t0 == 0 && group == 0 && w == 0 && lane == l && sq.over) atomicAdd(a.status, 1u);
 
-        // queries: row group * 32 BLK + 32 (w / 2) + n32 of the (token, head) pairs
-        const int row = group * 32 * BLK + 32 * (w >> 1) + n32, mrow = row < M ? row : M - 1;
-        const int tok = mrow / a.H;
-        const T* qlp = static_cast<const T*>(a.ql) + b * a.ql_b + tok * a.ql_t + (mrow - tok * a.H) * a.ql_h + 16 * half +
-                       8 * hf;
-        const T* qrp = static_cast<const T*>(a.qr) + b * a.qr_b + tok * a.qr_t + (mrow - tok * a.H) * a.qr_h + 16 * half +
-                       8 * hf;
-        // this wave's steps: every second one
-        auto load_q = [&](int s) { return 2 * s < DC / 16 ? load8(qlp + 32 * s) : load8(qrp + 32 * s - DC); };
-        Frag<T> qf[kKeepQ ? NS : 1];
+        // queries: row 16 WAVES group + 16 w + n of the (token, head) pairs
+        const int row = (group * WAVES + w) * 16 + (lane & 15), mrow = row < M ? row : M - 1;
+        const int tok = mrow / a.H, head = mrow - tok * a.H;
+        const T* qlp = static_cast<const T*>(a.ql) + b * a.ql_b + tok * a.ql_t + head * a.ql_h + 8 * (lane >> 4);
+        const T* qrp = static_cast<const T*>(a.qr) + b * a.qr_b + tok * a.qr_t + head * a.qr_h + 8 * (lane >> 4);
+        auto load_q = [&](int s) { return s < DC / 32 ? load8(qlp + 32 * s) : load8(qrp + 32 * s - DC); };
+        Frag<T> qf[kKeepQ ? NS - kLdsQ : 1];
         if constexpr (kKeepQ) {
 #pragma unroll
-            for (int s = 0; s < NS; ++s) qf[s] = load_q(s);
-        }
-        f32x16 acc[ND];
+            for (int s = 0; s < kLdsQ; ++s) lds_q[w][s][lane] = load_q(s);
 #pragma unroll
-        for (int d = 0; d < ND; ++d) acc[d] = zero16();
+            for (int s = kLdsQ; s < NS; ++s) qf[s - kLdsQ] = load_q(s);
+        }
+        f32x4 acc[2][ND];                                         // of this wave's rows, of the other wave's
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[0][d] = acc[1][d] = f32x4{0.f, 0.f, 0.f, 0.f};
         float m = -INFINITY, lsum = 0.f;
 
         // Page table entries of 64 pages, one per lane; -1 for no such page.
@@ -185,181 +261,230 @@ __global__ __launch_bounds__(128 * BLK, BLK > 2 ? 2 : 1) void mla_step_kernel(Ml
         // Issues tile t's loads; returns which of its halves exist.
         auto load = [&](int t, char* buf) -> int {
             const int k0 = t * kTile;
-            const int e0 = page(k0 >> ps);
-            int e1 = e0;
-            int64_t r0, r1;                                       // first cache row of each half
-            if (ps == 4) {
-                e1 = k0 + 16 < len ? page((k0 >> 4) + 1) : -1;    // a page not reached is not looked up
-                r0 = (int64_t)(e0 < 0 ? 0 : e0) << 4;
-                r1 = (int64_t)(e1 < 0 ? 0 : e1) << 4;
-            } else {
-                r0 = ((int64_t)(e0 < 0 ? 0 : e0) << ps) + (k0 & ((1 << ps) - 1));
-                r1 = r0 + 16;
-            }
-            const char* lo = static_cast<const char*>(a.cache) + r0 * (RC * 16);
-            const char* hi = static_cast<const char*>(a.cache) + r1 * (RC * 16);
-            const int have = (e0 >= 0) | (e1 >= 0) << 1;
+            int have = 0;
+            auto from = [&](int q) -> const char* {
+                const int k = k0 + 16 * q;
+                // entries past the length are not looked up
+                const int e = k < len ? page(k >> ps) : -1;
+                have |= (e >= 0) << q;
+                const int64_t r = ((int64_t)(e < 0 ? 0 : e) << ps) + (k & ((1 << ps) - 1));
+                return static_cast<const char*>(a.cache) + r * (RC * 16);
+            };
+            const char *lo = from(0), *hi = from(1);
             if (have == 3 && k0 + kTile <= len) load_cache_tile<RC, WAVES, false>(buf, lo, hi, 0, 0, w, lane);
-            else load_cache_tile<RC, WAVES, true>(buf, lo, hi, len - 1 - k0, have, w, lane);
+            else load_cache_tile<RC, WAVES, true>(buf, lo, hi, len - 1 - k0 < 31 ? len - 1 - k0 : 31, have, w, lane);
             return have;
         };
-        int have = load(t0, smem[0]), next_have = 0;
+        int have = load(t0, smem[0]), next = 0;
         wait_loads_and_lds();
         wg_barrier();
         for (int t = t0; t < t1; ++t) {
             const char* buf = smem[(t - t0) & 1];
-            if (t + 1 < t1) next_have = load(t + 1, smem[(t + 1 - t0) & 1]);
-            f32x16 sc = zero16();
+            if (t + 1 < t1) next = load(t + 1, smem[(t + 1 - t0) & 1]);
+            // LDS addresses are formed anew for each tile: kept over the loop,
+            // they push operands out of the registers
+            int ln = lane;
+            asm volatile("" : "+v"(ln));
+            const int g = ln >> 4;
+            f32x4 sc[2], odd[2];                                  // 16 keys each, in two chains
 #pragma unroll
-            for (int s = 0; s < NS; ++s) {
-                const Frag<T> kf = read_rows<T, RC>(buf, n32, 2 * s, hf, half);
-                sc = mma(kf, kKeepQ ? qf[kKeepQ ? s : 0] : load_q(s), sc);
+            for (int q = 0; q < 2; ++q) sc[q] = odd[q] = f32x4{0.f, 0.f, 0.f, 0.f};
+            {
+                // operands in the order of their use: for the steps whose
+                // queries are in LDS, these and the two blocks of keys, for
+                // the others the keys
+                Frag<T> q;
+                auto keys = [&](int s, int h) { return read_rows16<T, RC>(buf, 16 * h + (ln & 15), s, g); };
+                auto read = [&](int i) -> Frag<T> {
+                    if (i < 3 * kLdsQ) return i % 3 == 0 ? lds_q[w][kLdsQ ? i / 3 : 0][ln] : keys(i / 3, i % 3 - 1);
+                    return keys((i - kLdsQ) / 2, (i - kLdsQ) % 2);
+                };
+                ReadAhead<T, 2 * NS + kLdsQ, 6> ahead;
+                ahead.start(read);
+                ahead.template run<1, 1>(read, [&](int i, const Frag<T>& x) {
+                    if (i < 3 * kLdsQ && i % 3 == 0) {
+                        q = x;
+                        return;
+                    }
+                    const int s = i < 3 * kLdsQ ? i / 3 : (i - kLdsQ) / 2;
+                    const int h = i < 3 * kLdsQ ? i % 3 - 1 : (i - kLdsQ) % 2;
+                    if (i >= 3 * kLdsQ && h == 0) q = kKeepQ ? qf[kKeepQ ? s - kLdsQ : 0] : load_q(s);
+                    f32x4& y = s % 2 ? odd[h] : sc[h];
+                    y = mma16(x, q, y);
+                });
             }
 #pragma unroll
-            for (int g = 0; g < 4; ++g)
-                *reinterpret_cast<f32x4*>(part_sc[w][g][lane]) =
-                    f32x4{sc[4 * g], sc[4 * g + 1], sc[4 * g + 2], sc[4 * g + 3]};
-            __builtin_amdgcn_s_waitcnt(0xC07F);   // lgkmcnt(0): the sums are in LDS
-            wg_barrier();
+            for (int q = 0; q < 2; ++q)
 #pragma unroll
-            for (int g = 0; g < 4; ++g) {
-                const f32x4 x = *reinterpret_cast<const f32x4*>(part_sc[w ^ 1][g][lane]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) sc[4 * g + j] += x[j];
-            }
+                for (int r = 0; r < 4; ++r) sc[q][r] += odd[q][r];
             // keys that this lane's token sees in the tile: the first lim + 1
             const int k0 = t * kTile;
             if (k0 + kTile > len - a.Tq + 1 || have != 3) {
-                const int lim = len - a.Tq + tok - k0 - 4 * hf;
+                const int lim = len - a.Tq + tok - k0 - 4 * g;
 #pragma unroll
-                for (int r = 0; r < 16; ++r) {
-                    const int k = 8 * (r / 4) + r % 4;
-                    sc[r] = k > lim || !(have >> (r / 8) & 1) ? -INFINITY : sc[r];
-                }
+                for (int q = 0; q < 2; ++q)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r)
+                        sc[q][r] = 16 * q + r > lim || !(have >> q & 1) ? -INFINITY : sc[q][r];
             }
-            float mx = sc[0];
+            float mx = sc[0][0];
 #pragma unroll
-            for (int r = 1; r < 16; ++r) mx = fmaxf(mx, sc[r]);
-            mx = half_max(mx);
-            // The running maximum moves only when some row's grows by more
-            // than 2^8: until then its terms reach at most 2^8, exact enough
-            // in float32, and the output needs no rescaling (Dc / 4 products
-            // a lane and tile).
-            if (__any((mx - m) * c > 8.f || (m == -INFINITY && mx > -INFINITY))) {
-                const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.f : mn;
-                const float al = __builtin_amdgcn_exp2f((m - ms) * c);
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) mx = fmaxf(mx, sc[q][r]);
+            mx = group_max(mx);
+            // The running maximum moves only when it grows by more than 2^8
+            // (from -inf at first): until then its terms reach at most 2^8,
+            // exact enough in float32, and the output needs no rescaling.
+            float al = 1.f;
+            if ((mx - m) * c > 8.f) {
+                al = __builtin_amdgcn_exp2f((m - mx) * c);
                 lsum *= al;
+                m = mx;
+            }
+            const float mc = m == -INFINITY ? 0.f : m * c;        // nothing seen yet: all terms are 0
+            Frag<T> pf;
+#pragma unroll
+            for (int q = 0; q < 2; ++q)
+#pragma unroll
+                for (int r = 0; r < 4; ++r) {
+                    const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[q][r], c, -mc));
+                    lsum += p;
+                    pf[4 * q + r] = (T)p;      // bf16: the one rounding of the probabilities, as operands
+                }
+            probs[w][ln] = pf;
+            if (g == 0) factor[w][ln] = al;
+            wait_lds();
+            wg_barrier();
+            auto read = [&](int i) {
+                return read_cols16<T, RC>(buf + half * (DC / 2) * sizeof(T), 16 * i, ln);
+            };
+            ReadAhead<T, ND, 4> ahead;
+            ahead.start(read);
+            const Frag<T> po = probs[w ^ 1][ln];
+            const float ao = factor[w ^ 1][ln & 15];
+            if (__any(al != 1.f || ao != 1.f)) {
 #pragma unroll
                 for (int d = 0; d < ND; ++d)
 #pragma unroll
-                    for (int r = 0; r < 16; ++r) acc[d][r] *= al;
-                m = mn;
+                    for (int r = 0; r < 4; ++r) {
+                        acc[0][d][r] *= al;
+                        acc[1][d][r] *= ao;
+                    }
             }
-            const float mc = m == -INFINITY ? 0.f : m * c;
-            float ts = 0.f;
-#pragma unroll
-            for (int r = 0; r < 16; ++r) {
-                sc[r] = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r], c, -mc));
-                ts += sc[r];
-            }
-            lsum += ts;
-#pragma unroll
-            for (int s = 0; s < 2; ++s) {
-                const Frag<T> pf = to_frag<T>(sc, s);
-#pragma unroll
-                for (int d = 0; d < ND; ++d)
-                    acc[d] = mma(read_cols<T, RC>(buf + half * (DC / 2) * sizeof(T), 16 * s, 32 * d, lane), pf, acc[d]);
-            }
-            have = next_have;
+            ahead.template run<2>(read, [&](int i, const Frag<T>& x) {
+                acc[0][i] = mma16(x, pf, acc[0][i]);
+                acc[1][i] = mma16(x, po, acc[1][i]);
+            });
+            have = next;
             wait_loads_and_lds();
             wg_barrier();
         }
-        const float lt = half_sum(lsum);
-        int ln = lane;
-        asm volatile("" : "+v"(ln));                              // formed again here, not kept over the loop
-        const int orow = group * 32 * BLK + 32 * (w >> 1) + (ln & 31);
-        const bool live = orow < M;
+        const float lt = group_sum(lsum);
+        int ln = lane;                                            // the same here
+        asm volatile("" : "+v"(ln));
+        const int g = ln >> 4, r0 = (group * WAVES + w) * 16 + (ln & 15), r1 = r0 + (half ? -16 : 16);
         if (t0 == 0 && t1 == tiles) {
-            const float inv = lt > 0.f ? 1.f / lt : lt == 0.f ? 0.f : lt;
-            const int64_t at_o = (int64_t)b * M + (live ? orow : M - 1);
-            T* op = static_cast<T*>(a.o) + at_o * DC + half * (DC / 2);
+            const float inv = lt > 0.f ? 1.f / lt : lt == 0.f ? 0.f : lt;   // no visible key: 0; NaN stays NaN
+            if (g == 0) factor[w][ln] = inv;
+            wait_lds();
+            wg_barrier();
+            const float io = factor[w ^ 1][ln & 15];
+            T* op = static_cast<T*>(a.o) + (int64_t)b * M * DC + half * (DC / 2) + 4 * g;
 #pragma unroll
-            for (int d = 0; d < ND; ++d) store_tile<T>(op + 32 * d, acc[d], inv, hf, live);
-            if (a.lse && live && hf == 0 && half == 0)
-                a.lse[at_o] = lt == 0.f ? -INFINITY : (m * c + __builtin_amdgcn_logf(lt)) * 0.6931471805599453f;
+            for (int d = 0; d < ND; ++d) {
+                if (r0 < M) store4(op + (int64_t)r0 * DC + 16 * d, acc[0][d], inv);
+                if (r1 < M) store4(op + (int64_t)r1 * DC + 16 * d, acc[1][d], io);
+            }
+            if (a.lse && r0 < M && g == 0)
+                a.lse[(int64_t)b * M + r0] =
+                    lt == 0.f ? -INFINITY : (m * c + __builtin_amdgcn_logf(lt)) * 0.6931471805599453f;
+            wait_lds();
+            wg_barrier();                                         // the next sequence writes factor again
         } else {
-            float* p = partial(a, group, part, t0 > 0 ? 0 : 1, 32 * (w >> 1) + (ln & 31));
-            if (hf == 0 && half == 0) {
+            const int j = t0 > 0 ? 0 : 1;
+            float* p = partial(a, group, part, j, 16 * w + (ln & 15));
+            float* x = partial(a, group, part, j, 16 * (w ^ 1) + (ln & 15));
+            if (g == 0) {
                 p[0] = m * c;
                 p[1] = lt;
             }
 #pragma unroll
-            for (int d = 0; d < ND; ++d) store_tile<float>(p + 4 + half * (DC / 2) + 32 * d, acc[d], 1.f, hf, true);
+            for (int d = 0; d < ND; ++d) {
+                store4(p + 4 + half * (DC / 2) + 16 * d + 4 * g, acc[0][d], 1.f);
+                store4(x + 4 + half * (DC / 2) + 16 * d + 4 * g, acc[1][d], 1.f);
+            }
         }
     }
 }
 
-// Joins the parts of a row of queries; writes zeros for rows of sequences
-// without cache rows. A workgroup takes one row: its four waves take the parts
-// in turn, each over all columns, and their sums meet in LDS.
-template <class T, int DC> __global__ __launch_bounds__(256) void mla_step_join_kernel(MlaStepArgs a) {
+// Joins the parts of sequences that span several; writes zeros for sequences
+// without cache rows. A workgroup takes a.join_rows rows of queries of one
+// sequence, one after the other: its four waves take the parts in turn, each
+// over all columns, and their sums meet in LDS.
+template <class T, int DC> __global__ __launch_bounds__(256) void mla_step_join_kernel(MlaStepArgs a, int blocks) {
     __shared__ __attribute__((aligned(16))) float sums[4][DC];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-    const int M = a.Tq * a.H, b = blockIdx.x / M, row = blockIdx.x % M;
+    const int M = a.Tq * a.H, b = blockIdx.x / blocks, row0 = blockIdx.x % blocks * a.join_rows;
+    const int row1 = row0 + a.join_rows < M ? row0 + a.join_rows : M;
     int first = 0, total = 0, tiles = 0;
     for (int b0 = 0; b0 < a.Nb; b0 += 64) {
-        int cnt;
-        const int sum = scan_tiles(a, b0, lane, cnt);
+        const Scan sq = scan_tiles(a, b0, lane);
         if (b >= b0 && b < b0 + 64) {
-            tiles = __builtin_amdgcn_readlane(cnt, b - b0);
-            first = total + __builtin_amdgcn_readlane(sum, b - b0) - tiles;
+            tiles = __builtin_amdgcn_readlane(sq.cnt, b - b0);
+            first = total + __builtin_amdgcn_readlane(sq.sum, b - b0) - tiles;
         }
-        total += __builtin_amdgcn_readlane(sum, 63);
+        total += sq.all();
     }
-    T* op = static_cast<T*>(a.o) + (int64_t)blockIdx.x * DC;
+    T* op = static_cast<T*>(a.o) + ((int64_t)b * M + row0) * DC;
+    float* lp = a.lse ? a.lse + (int64_t)b * M : nullptr;
     if (tiles == 0) {
-        for (int d = threadIdx.x; d < DC; d += 256) op[d] = (T)0.f;
-        if (a.lse && threadIdx.x == 0) a.lse[blockIdx.x] = -INFINITY;
+        for (int d = threadIdx.x; d < (row1 - row0) * DC; d += 256) op[d] = (T)0.f;
+        if (lp)
+            for (int i = row0 + threadIdx.x; i < row1; i += 256) lp[i] = -INFINITY;
         return;
     }
     const int per = part_tiles(a, total), p0 = first / per, p1 = (first + tiles - 1) / per;
     if (p0 == p1) return;
-    const int group = row / (32 * a.blocks), r = row % (32 * a.blocks);
-    float m = -INFINITY;
-    for (int p = p0 + lane; p <= p1; p += 64) m = fmaxf(m, partial(a, group, p, p > p0 ? 0 : 1, r)[0]);
+    for (int row = row0; row < row1; ++row, op += DC) {
+        const int group = row / (16 * a.waves), r = row % (16 * a.waves);
+        float m = -INFINITY;
+        for (int p = p0 + lane; p <= p1; p += 64) m = fmaxf(m, partial(a, group, p, p > p0 ? 0 : 1, r)[0]);
 #pragma unroll
-    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-    const float ms = m == -INFINITY ? 0.f : m;
-    float l = 0.f;
-    for (int p = p0 + lane; p <= p1; p += 64) {
-        const float* x = partial(a, group, p, p > p0 ? 0 : 1, r);
-        l += x[1] * __builtin_amdgcn_exp2f(x[0] - ms);
-    }
-#pragma unroll
-    for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
-    constexpr int V = DC / 256;
-    f32x4 s[V];
-#pragma unroll
-    for (int v = 0; v < V; ++v) s[v] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-    for (int p = p0 + w; p <= p1; p += 4) {
-        const float* x = partial(a, group, p, p > p0 ? 0 : 1, r);
-        const float f = __builtin_amdgcn_exp2f(x[0] - ms);
-#pragma unroll
-        for (int v = 0; v < V; ++v) {
-            const f32x4 y = *reinterpret_cast<const f32x4*>(x + 4 + 256 * v + 4 * lane);
-#pragma unroll
-            for (int j = 0; j < 4; ++j) s[v][j] += f * y[j];
+        for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+        const float ms = m == -INFINITY ? 0.f : m;
+        float l = 0.f;
+        for (int p = p0 + lane; p <= p1; p += 64) {
+            const float* x = partial(a, group, p, p > p0 ? 0 : 1, r);
+            l += x[1] * __builtin_amdgcn_exp2f(x[0] - ms);
         }
-    }
 #pragma unroll
-    for (int v = 0; v < V; ++v) *reinterpret_cast<f32x4*>(&sums[w][256 * v + 4 * lane]) = s[v];
-    __syncthreads();
-    const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
-    for (int d = threadIdx.x; d < DC; d += 256)
-        op[d] = (T)((((sums[0][d] + sums[1][d]) + sums[2][d]) + sums[3][d]) * inv);
-    if (a.lse && threadIdx.x == 0)
-        a.lse[blockIdx.x] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+        for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+        constexpr int V = DC / 256;
+        f32x4 s[V];
+#pragma unroll
+        for (int v = 0; v < V; ++v) s[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int p = p0 + w; p <= p1; p += 4) {
+            const float* x = partial(a, group, p, p > p0 ? 0 : 1, r);
+            const float f = __builtin_amdgcn_exp2f(x[0] - ms);
+#pragma unroll
+            for (int v = 0; v < V; ++v) {
+                const f32x4 y = *reinterpret_cast<const f32x4*>(x + 4 + 256 * v + 4 * lane);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) s[v][j] += f * y[j];
+            }
+        }
+#pragma unroll
+        for (int v = 0; v < V; ++v) *reinterpret_cast<f32x4*>(&sums[w][256 * v + 4 * lane]) = s[v];
+        __syncthreads();
+        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+        for (int d = threadIdx.x; d < DC; d += 256)
+            op[d] = (T)((((sums[0][d] + sums[1][d]) + sums[2][d]) + sums[3][d]) * inv);
+        if (lp && threadIdx.x == 0)
+            lp[row] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+        __syncthreads();
+    }
 }
 
 // One thread per 16-byte chunk of a new token.
@@ -403,15 +528,14 @@ template <class T> __global__ __launch_bounds__(256) void mla_append_kernel(MlaA
 
 template <class T, int DC, int DR> hipError_t launch(const MlaStepArgs& a, hipStream_t s) {
     const dim3 grid((unsigned)(a.groups * a.parts));
-    if (a.blocks == 1) mla_step_kernel<T, DC, DR, 1><<<grid, 128, 0, s>>>(a);
-    else if (a.blocks == 2) mla_step_kernel<T, DC, DR, 2><<<grid, 256, 0, s>>>(a);
-    if constexpr (max_blocks<T, DC>() > 2) {
-        if (a.blocks == 3) mla_step_kernel<T, DC, DR, 3><<<grid, 384, 0, s>>>(a);
-        else if (a.blocks == 4) mla_step_kernel<T, DC, DR, 4><<<grid, 512, 0, s>>>(a);
-    }
+    if (a.waves == 2) mla_step_kernel<T, DC, DR, 2><<<grid, 128, 0, s>>>(a);
+    else if (a.waves == 4) mla_step_kernel<T, DC, DR, 4><<<grid, 256, 0, s>>>(a);
+    else if (a.waves == 6) mla_step_kernel<T, DC, DR, 6><<<grid, 384, 0, s>>>(a);
+    else if constexpr (max_waves<T, DC>() > 6) mla_step_kernel<T, DC, DR, 8><<<grid, 512, 0, s>>>(a);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
-    mla_step_join_kernel<T, DC><<<dim3((unsigned)((int64_t)a.Nb * a.Tq * a.H)), 256, 0, s>>>(a);
+    const int blocks = (a.Tq * a.H + a.join_rows - 1) / a.join_rows;
+    mla_step_join_kernel<T, DC><<<dim3((unsigned)((int64_t)a.Nb * blocks)), 256, 0, s>>>(a, blocks);
     return hipGetLastError();
 }
 template <class T> hipError_t launch_dims(const MlaStepArgs& a, hipStream_t s) {
@@ -421,24 +545,25 @@ template <class T> hipError_t launch_dims(const MlaStepArgs& a, hipStream_t s) {
 
 }  // namespace
 
-// The split over workgroups. A block of 32 rows of queries costs the same
-// whether its rows are used, so the blocks are spread evenly over as few
-// groups as hold them. One workgroup of three or four blocks fills a compute
-// unit, two of one block fit.
+// The split over workgroups. The blocks of 32 rows of queries are spread evenly
+// over as few groups as hold them, two waves a block.
 size_t mla_step_plan(MlaStepArgs& a) {
-    const int64_t blocks = ((int64_t)a.Tq * a.H + 31) / 32;
-    const int64_t most_blocks = a.bf16 ? 4 : a.Dc == 512 ? max_blocks<float, 512>() : max_blocks<float, 256>();
+    const int64_t rows = (int64_t)a.Tq * a.H, blocks = (rows + 31) / 32;
+    const int most_blocks = (!a.bf16 && a.Dc == 512 ? max_waves<float, 512>() : 8) / 2;
     a.groups = (int32_t)((blocks + most_blocks - 1) / most_blocks);
-    a.blocks = (int32_t)((blocks + a.groups - 1) / a.groups);
+    a.waves = (int32_t)((blocks + a.groups - 1) / a.groups) * 2;
     const int64_t most = (int64_t)a.Nb * ((((int64_t)a.max_pages << a.page_shift) + kTile - 1) / kTile);
-    int64_t parts = (a.blocks == 1 ? 512 : 256) / a.groups;
+    int64_t parts = 256 / a.groups;
     if (parts < 32) parts = 32;
     if (parts > most) parts = most;
     a.parts = (int32_t)(parts > 1 ? parts : 1);
     // writing and joining a part's results, in tiles: about 1/16 a tile for 96
     // rows of 512 columns; the sum of both costs is least at sqrt(total) / 4
     a.part_cost = 0.25f;
-    return (size_t)a.groups * a.parts * 2 * (32 * a.blocks) * (a.Dc + 4) * sizeof(float);
+    // the join: about 1024 workgroups, most of which find nothing to join
+    const int64_t j = (a.Nb * rows + 1023) / 1024;
+    a.join_rows = (int32_t)(j < rows ? j : rows);
+    return (size_t)a.groups * a.parts * 2 * (16 * a.waves) * (a.Dc + 4) * sizeof(float);
 }
 
 hipError_t launch_mla_step(const MlaStepArgs& a, hipStream_t s) {

@@ -48,10 +48,25 @@ __device__ __forceinline__ f32x4 mma16(f32x8 a, f32x8 b, f32x4 c) {
     for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_16x16x4f32(a[j], b[j], c, 0, 0, 0);
     return c;
 }
+// The position of a tile's chunks: chunk c of row r lies at c ^ swizzle16(r).
+// LDS serves a read of 16 bytes per lane in quarters of 16 lanes, of which one
+// is the lanes 0-3, 12-15 and 20-27: here rows 0-3 and 12-15 of a group's chunk
+// and rows 4-11 of its neighbour's. It serves the transposed read of 8 bytes
+// per lane in halves: chunk pairs of eight consecutive rows. float32's column
+// read takes four chunks of four rows, four rows apart. Each of these takes
+// every bank once.
+template <class T, int RC> __device__ __forceinline__ int swizzle16(int r) {
+    if constexpr (sizeof(T) == 4) {
+        static_assert(RC % 16 == 0, "whole bank cycles");
+        return r & 15;
+    } else {
+        return RC % 16 == 0 ? (r & 7) << 1 : r & 6;   // 8 mod 16: odd rows are half a bank cycle away already
+    }
+}
 // A operand over the columns: tile row r, columns 32 step + 8 g .. + 7
 template <class T, int RC> __device__ __forceinline__ Frag<T> read_rows16(const char* lds, int r, int step, int g) {
     const char* p = lds + r * (RC * 16);
-    const int sw = swizzle<RC>(r);
+    const int sw = swizzle16<T, RC>(r);
     if constexpr (sizeof(T) == 2) {
         return *reinterpret_cast<const bf16x8*>(p + chunk_at<RC>(4 * step, g, sw));
     } else {
@@ -68,7 +83,7 @@ template <class T, int RC> __device__ __forceinline__ Frag<T> read_cols16(const 
 #pragma unroll
         for (int u = 0; u < 2; ++u) {
             const int r = 16 * u + 4 * g + ((lane >> 2) & 3);
-            const char* p = lds + r * (RC * 16) + (lane & 1) * 8 + chunk_at<RC>(col0 >> 3, (lane & 3) >> 1, swizzle<RC>(r));
+            const char* p = lds + r * (RC * 16) + (lane & 1) * 8 + chunk_at<RC>(col0 >> 3, (lane & 3) >> 1, swizzle16<T, RC>(r));
             const bf16x4 b = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((KDA_LDS s16x4*)p));
 #pragma unroll
             for (int j = 0; j < 4; ++j) f[4 * u + j] = b[j];
@@ -80,7 +95,7 @@ template <class T, int RC> __device__ __forceinline__ Frag<T> read_cols16(const 
         for (int j = 0; j < 8; ++j) {
             const int r = 16 * (j >> 2) + 4 * g + (j & 3);
             f[j] = *reinterpret_cast<const float*>(lds + r * (RC * 16) + (lane & 3) * 4 +
-                                                   chunk_at<RC>(col0 >> 2, (lane & 15) >> 2, swizzle<RC>(r)));
+                                                   chunk_at<RC>(col0 >> 2, (lane & 15) >> 2, swizzle16<T, RC>(r)));
         }
         return f;
     }
@@ -145,7 +160,7 @@ __device__ __forceinline__ float* partial(const MlaStepArgs& a, int group, int p
 // EDGE, rows past rmax are not read (row rmax stands in), and halves whose
 // page does not exist (bits of have) are zeros: a hidden row's weight is 0, but
 // what it multiplies has to be finite.
-template <int RC, int WAVES, bool EDGE>
+template <class T, int RC, int WAVES, bool EDGE>
 __device__ __forceinline__ void load_cache_tile(char* lds, const char* lo, const char* hi, int rmax, int have, int w,
                                                 int lane) {
     constexpr int kInstr = 16 * RC / 64;
@@ -161,7 +176,7 @@ __device__ __forceinline__ void load_cache_tile(char* lds, const char* lo, const
         } else {                                          // a row has RC / 8 groups of 8 chunks
             r = (int)((8u * (unsigned)j + ((unsigned)lane >> 3)) / (unsigned)(RC / 8));
         }
-        const int src = s ^ swizzle<RC>(r);
+        const int src = s ^ swizzle16<T, RC>(r);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
             char* to = lds + (q * kInstr + j) * 1024;
@@ -271,8 +286,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
                 return static_cast<const char*>(a.cache) + r * (RC * 16);
             };
             const char *lo = from(0), *hi = from(1);
-            if (have == 3 && k0 + kTile <= len) load_cache_tile<RC, WAVES, false>(buf, lo, hi, 0, 0, w, lane);
-            else load_cache_tile<RC, WAVES, true>(buf, lo, hi, len - 1 - k0 < 31 ? len - 1 - k0 : 31, have, w, lane);
+            if (have == 3 && k0 + kTile <= len) load_cache_tile<T, RC, WAVES, false>(buf, lo, hi, 0, 0, w, lane);
+            else load_cache_tile<T, RC, WAVES, true>(buf, lo, hi, len - 1 - k0 < 31 ? len - 1 - k0 : 31, have, w, lane);
             return have;
         };
         int have = load(t0, smem[0]), next = 0;

@@ -149,8 +149,9 @@ template <class T, int N, int AHEAD> struct ReadAhead {
         for (int i = 0; i < kAhead; ++i) ring[i] = read(i);
         __builtin_amdgcn_sched_barrier(0);
     }
-    // MMAS products with each operand of READS LDS reads
-    template <int MMAS = 1, int READS = 2, class Read, class Use> __device__ __forceinline__ void run(Read read, Use use) {
+    // MMAS products with each operand of READS LDS reads, of which has(i) has any
+    template <int MMAS = 1, int READS = 2, class Read, class Use, class Has>
+    __device__ __forceinline__ void run(Read read, Use use, Has has) {
         __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
         for (int i = 0; i < N; ++i) {
@@ -160,11 +161,14 @@ template <class T, int N, int AHEAD> struct ReadAhead {
         if constexpr (sizeof(T) == 2) {
 #pragma unroll
             for (int i = 0; i < N - kAhead; ++i) {
-                __builtin_amdgcn_sched_group_barrier(0x008, MMAS, 0);
+                if (has(i)) __builtin_amdgcn_sched_group_barrier(0x008, MMAS, 0);
                 __builtin_amdgcn_sched_group_barrier(0x100, READS, 0);
             }
         }
         __builtin_amdgcn_sched_barrier(0);
+    }
+    template <int MMAS = 1, int READS = 2, class Read, class Use> __device__ __forceinline__ void run(Read read, Use use) {
+        run<MMAS, READS>(read, use, [](int) { return true; });
     }
 };
 

@@ -203,7 +203,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
     // is under way: the first kLdsQ steps' of bf16 stay in LDS, and float32's
     // are read again for every tile (its products take 16 times as long).
     constexpr bool kKeepQ = sizeof(T) == 2;
-    constexpr int kLdsQ = kKeepQ && DC == 512 ? 6 : 0;
+    constexpr int kLdsQ = kKeepQ && DC == 512 ? 7 : 0;
     __shared__ __attribute__((aligned(1024))) char smem[2][kBuf];
     // what the two waves of a row block tell each other: probabilities as
     // operands, the factor of the running maximum's move (later 1 / sum)
@@ -326,7 +326,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
                     if (i >= 3 * kLdsQ && h == 0) q = kKeepQ ? qf[kKeepQ ? s - kLdsQ : 0] : load_q(s);
                     f32x4& y = s % 2 ? odd[h] : sc[h];
                     y = mma16(x, q, y);
-                });
+                }, [](int i) { return i >= 3 * kLdsQ || i % 3 != 0; });
             }
 #pragma unroll
             for (int q = 0; q < 2; ++q)

@@ -71,7 +71,7 @@ template <int RC> __device__ __forceinline__ int swizzle(int r) {
 // 16 bytes per lane from global memory to LDS at `lds` (uniform) + 16 * lane.
 // Written as an instruction so that the compiler, which cannot tell the two
 // buffers apart, does not wait for the next tile before it reads this one;
-// wait_loads() and the barrier order them. It has no register output.
+// wait_loads_and_lds() and the barrier order them. It has no register output.
 __device__ __forceinline__ void load_lds16(const char* g, char* lds) {
     const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(KDA_LDS char*)lds);
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(base), "v"(g) : "memory");
@@ -83,6 +83,18 @@ __device__ __forceinline__ void load_lds16s(const char* g, int off, char* lds) {
     const uint64_t from = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32 |
                           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u);
     asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, %2" ::"s"(base), "v"(off), "s"(from) : "memory");
+}
+// the same where `on` (uniform): no branch, which would end the compiler's
+// scheduling region. All lanes of the wave are active here.
+__device__ __forceinline__ void load_lds16s_if(bool on, const char* g, int off, char* lds) {
+    const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(KDA_LDS char*)lds);
+    const uint64_t u = reinterpret_cast<uint64_t>(g);
+    const uint64_t from = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32 |
+                          (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u);
+    const uint32_t lanes = __builtin_amdgcn_readfirstlane(on ? 0xffffffffu : 0u);
+    asm volatile("s_mov_b32 m0, %0\n\ts_mov_b32 exec_lo, %3\n\ts_mov_b32 exec_hi, %3\n\t"
+                 "global_load_lds_dwordx4 %1, %2\n\ts_mov_b64 exec, -1" ::"s"(base), "v"(off), "s"(from), "s"(lanes)
+                 : "memory");
 }
 
 // Rows [0, ROWS) of a tile from global rows `stride` bytes apart to LDS, WAVES

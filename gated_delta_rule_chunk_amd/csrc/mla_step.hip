@@ -154,42 +154,52 @@ __device__ __forceinline__ float* partial(const MlaStepArgs& a, int group, int p
     return a.part + ((((int64_t)group * a.parts + part) * 2 + j) * (16 * a.waves) + row) * (a.Dc + 4);
 }
 
-// A tile's rows of RC chunks to LDS (layout: mla_common.hpp), 16 consecutive
-// cache rows from each of two addresses. Lane l of a half's instruction j fills chunk 64 j + l of it; as a row's chunks are permuted within their
-// groups only, its source is that chunk with its low bits exchanged. With
-// EDGE, rows past rmax are not read (row rmax stands in), and halves whose
-// page does not exist (bits of have) are zeros: a hidden row's weight is 0, but
-// what it multiplies has to be finite.
-template <class T, int RC, int WAVES, bool EDGE>
-__device__ __forceinline__ void load_cache_tile(char* lds, const char* lo, const char* hi, int rmax, int have, int w,
-                                                int lane) {
-    constexpr int kInstr = 16 * RC / 64;
+// A tile's rows of RC chunks come to LDS (layout: mla_common.hpp) as two halves
+// of 16 consecutive cache rows. Lane l of a half's instruction j fills chunk
+// 64 j + l of it; as a row's chunks are permuted within their groups only, its
+// source is that chunk with its low bits exchanged.
+template <class T, int RC> struct CacheTile {
+    static constexpr int kInstr = 16 * RC / 64;           // a half
+    static __device__ __forceinline__ int row(int j, int lane) {
+        if constexpr (RC % 64 == 0) return j / (RC / 64); // an instruction stays in one row
+        // a row has RC / 8 groups of 8 chunks
+        return (int)((8u * (unsigned)j + ((unsigned)lane >> 3)) / (unsigned)(RC / 8));
+    }
+    static __device__ __forceinline__ int source(int j, int lane) {
+        return (j * 64 + lane) ^ swizzle16<T, RC>(row(j, lane));
+    }
+};
+// Loads a wave issues for a tile, and the x-th of them, if `on`: for a tile whose
+// rows all exist.
+template <class T, int RC, int WAVES> constexpr int tile_loads() {
+    return (CacheTile<T, RC>::kInstr + WAVES - 1) / WAVES * 2;
+}
+template <class T, int RC, int WAVES>
+__device__ __forceinline__ void load_of_tile(int x, bool on, char* lds, const char* lo, const char* hi, int w, int lane) {
+    using C = CacheTile<T, RC>;
+    const int q = x & 1, j = (x >> 1) * WAVES + w;
+    load_lds16s_if(on && (C::kInstr % WAVES == 0 || j < C::kInstr), q ? hi : lo, C::source(j, lane) * 16,
+                   lds + (q * C::kInstr + j) * 1024);
+}
+// A whole tile of which rows past rmax are not read (row rmax stands in), and
+// halves whose page does not exist (bits of have) are zeros: a hidden row's
+// weight is 0, but what it multiplies has to be finite.
+template <class T, int RC, int WAVES>
+__device__ __forceinline__ void load_edge_tile(char* lds, const char* lo, const char* hi, int rmax, int have, int w,
+                                               int lane) {
+    using C = CacheTile<T, RC>;
     asm volatile("" : "+v"(lane));   // addresses are formed here for each tile, not kept in registers
-#pragma unroll
-    for (int k = 0; k < (kInstr + WAVES - 1) / WAVES; ++k) {
-        const int j = k * WAVES + w;
-        if (kInstr % WAVES != 0 && j >= kInstr) break;
-        const int s = j * 64 + lane;
-        int r;
-        if constexpr (RC % 64 == 0) {                     // an instruction stays in one row
-            r = j / (RC / 64);
-        } else {                                          // a row has RC / 8 groups of 8 chunks
-            r = (int)((8u * (unsigned)j + ((unsigned)lane >> 3)) / (unsigned)(RC / 8));
-        }
-        const int src = s ^ swizzle16<T, RC>(r);
+    for (int j = w; j < C::kInstr; j += WAVES) {
+        const int src = C::source(j, lane), r = C::row(j, lane);
 #pragma unroll
         for (int q = 0; q < 2; ++q) {
-            char* to = lds + (q * kInstr + j) * 1024;
-            if constexpr (EDGE) {
-                const int f = 16 * q <= rmax ? q : 0;              // the half its rows come from
-                if (have >> f & 1) {
-                    const int last = rmax - 16 * f, rr = f < q || r > last ? last : r;
-                    load_lds16((f ? hi : lo) + (src + (rr - r) * RC) * 16, to);
-                } else {
-                    *reinterpret_cast<u32x4*>(to + lane * 16) = u32x4{0, 0, 0, 0};
-                }
+            char* to = lds + (q * C::kInstr + j) * 1024;
+            const int f = 16 * q <= rmax ? q : 0;         // the half its rows come from
+            if (have >> f & 1) {
+                const int last = rmax - 16 * f, rr = f < q || r > last ? last : r;
+                load_lds16((f ? hi : lo) + (src + (rr - r) * RC) * 16, to);
             } else {
-                load_lds16s(q ? hi : lo, src * 16, to);
+                *reinterpret_cast<u32x4*>(to + lane * 16) = u32x4{0, 0, 0, 0};
             }
         }
     }
@@ -203,7 +213,11 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
     // is under way: the first kLdsQ steps' of bf16 stay in LDS, and float32's
     // are read again for every tile (its products take 16 times as long).
     constexpr bool kKeepQ = sizeof(T) == 2;
-    constexpr int kLdsQ = kKeepQ && DC == 512 ? 7 : 0;
+    constexpr int kLdsQ = kKeepQ && DC == 512 ? 8 : 0;
+    // bf16: the next tile's loads go out one by one under the products of the
+    // scores. All at once, a wave waits about 150 clocks for each. float32's
+    // products leave no registers for them, and take far longer than the loads.
+    constexpr bool kSpread = sizeof(T) == 2;
     __shared__ __attribute__((aligned(1024))) char smem[2][kBuf];
     // what the two waves of a row block tell each other: probabilities as
     // operands, the factor of the running maximum's move (later 1 / sum)
@@ -244,6 +258,61 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
         const T* qlp = static_cast<const T*>(a.ql) + b * a.ql_b + tok * a.ql_t + head * a.ql_h + 8 * (lane >> 4);
         const T* qrp = static_cast<const T*>(a.qr) + b * a.qr_b + tok * a.qr_t + head * a.qr_h + 8 * (lane >> 4);
         auto load_q = [&](int s) { return s < DC / 32 ? load8(qlp + 32 * s) : load8(qrp + 32 * s - DC); };
+        f32x4 acc[2][ND];                                         // of this wave's rows, of the other wave's
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[0][d] = acc[1][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float m = -INFINITY, lsum = 0.f;
+
+        // A tile: which of its halves exist, where they lie, whether all its rows do
+        struct Tile {
+            int have;
+            bool whole;
+            const char *lo, *hi;
+        };
+        // Page table entries of 64 pages, one per lane; -1 for no such page or one
+        // past the length. A tile's halves lie in one page or, where pages have
+        // 16 rows, in an even one and the next: of the same 64.
+        const int32_t* table = a.table + (int64_t)b * a.max_pages;
+        int pbase = -64, pages = 0;
+        auto find = [&](int t) {
+            const int k0 = t * kTile, p = k0 >> ps;
+            if (p >= pbase + 64) {
+                pbase = p;
+                const int i = p + lane;
+                const int64_t r = (int64_t)i << ps;
+                int e = i < a.max_pages && r < len ? table[i] : 0;
+                if (e < 0 || e >= a.n_pages) e = -1;
+                // counted once: where the page's first row is this part's
+                const uint64_t bad = __ballot(e < 0 && r >= t0 * kTile && r < (int64_t)t1 * kTile);
+                if (bad && group == 0 && w == 0 && lane == 0) atomicAdd(a.status, (unsigned)__popcll(bad));
+                pages = r < len ? e : -1;
+            }
+            const int e0 = __builtin_amdgcn_readlane(pages, p - pbase);
+            const int e1 = __builtin_amdgcn_readlane(pages, ((k0 + 16) >> ps) - pbase);
+            const int mask = (1 << ps) - 1;
+            Tile x;
+            x.have = (e0 >= 0 ? 1 : 0) | (e1 >= 0 ? 2 : 0);
+            x.whole = x.have == 3 && k0 + kTile <= len;
+            // (a missing page's address is not used)
+            x.lo = static_cast<const char*>(a.cache) + (((int64_t)e0 << ps) + (k0 & mask)) * (RC * 16);
+            x.hi = static_cast<const char*>(a.cache) + (((int64_t)e1 << ps) + ((k0 + 16) & mask)) * (RC * 16);
+            return x;
+        };
+        auto load_edge = [&](const Tile& x, int t, char* to) {
+            const int rmax = len - 1 - t * kTile;
+            load_edge_tile<T, RC, WAVES>(to, x.lo, x.hi, rmax < kTile - 1 ? rmax : kTile - 1, x.have, w, lane);
+        };
+        constexpr int kLoads = tile_loads<T, RC, WAVES>();
+        auto load_whole = [&](const Tile& x, char* to) {
+            int ln = lane;
+            asm volatile("" : "+v"(ln));                          // addresses are formed here, not kept in registers
+#pragma unroll
+            for (int i = 0; i < kLoads; ++i) load_of_tile<T, RC, WAVES>(i, true, to, x.lo, x.hi, w, ln);
+        };
+        Tile next = find(t0);
+        if (next.whole) load_whole(next, smem[0]);
+        else load_edge(next, t0, smem[0]);
+        int have = next.have;
         Frag<T> qf[kKeepQ ? NS - kLdsQ : 1];
         if constexpr (kKeepQ) {
 #pragma unroll
@@ -251,51 +320,17 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
 #pragma unroll
             for (int s = kLdsQ; s < NS; ++s) qf[s - kLdsQ] = load_q(s);
         }
-        f32x4 acc[2][ND];                                         // of this wave's rows, of the other wave's
-#pragma unroll
-        for (int d = 0; d < ND; ++d) acc[0][d] = acc[1][d] = f32x4{0.f, 0.f, 0.f, 0.f};
-        float m = -INFINITY, lsum = 0.f;
-
-        // Page table entries of 64 pages, one per lane; -1 for no such page.
-        const int32_t* table = a.table + (int64_t)b * a.max_pages;
-        int pbase = -64, pages = 0;
-        auto page = [&](int p) -> int {
-            if (p >= pbase + 64) {
-                pbase = p;
-                const int i = p + lane;
-                int e = i < a.max_pages ? table[i] : -1;
-                if (e < 0 || e >= a.n_pages) e = -1;
-                // counted once: where the page's first row is this part's
-                const int64_t r = (int64_t)i << ps;
-                const uint64_t bad = __ballot(e < 0 && r < len && r >= t0 * kTile && r < (int64_t)t1 * kTile);
-                if (bad && group == 0 && w == 0 && lane == 0) atomicAdd(a.status, (unsigned)__popcll(bad));
-                pages = e;
-            }
-            return __builtin_amdgcn_readlane(pages, p - pbase);
-        };
-        // Issues tile t's loads; returns which of its halves exist.
-        auto load = [&](int t, char* buf) -> int {
-            const int k0 = t * kTile;
-            int have = 0;
-            auto from = [&](int q) -> const char* {
-                const int k = k0 + 16 * q;
-                // entries past the length are not looked up
-                const int e = k < len ? page(k >> ps) : -1;
-                have |= (e >= 0) << q;
-                const int64_t r = ((int64_t)(e < 0 ? 0 : e) << ps) + (k & ((1 << ps) - 1));
-                return static_cast<const char*>(a.cache) + r * (RC * 16);
-            };
-            const char *lo = from(0), *hi = from(1);
-            if (have == 3 && k0 + kTile <= len) load_cache_tile<T, RC, WAVES, false>(buf, lo, hi, 0, 0, w, lane);
-            else load_cache_tile<T, RC, WAVES, true>(buf, lo, hi, len - 1 - k0 < 31 ? len - 1 - k0 : 31, have, w, lane);
-            return have;
-        };
-        int have = load(t0, smem[0]), next = 0;
         wait_loads_and_lds();
         wg_barrier();
         for (int t = t0; t < t1; ++t) {
             const char* buf = smem[(t - t0) & 1];
-            if (t + 1 < t1) next = load(t + 1, smem[(t + 1 - t0) & 1]);
+            char* const to = smem[(t + 1 - t0) & 1];
+            next.whole = false;
+            if (t + 1 < t1) {
+                next = find(t + 1);
+                if (!next.whole) load_edge(next, t + 1, to);
+                else if (!kSpread) load_whole(next, to);
+            }
             // LDS addresses are formed anew for each tile: kept over the loop,
             // they push operands out of the registers
             int ln = lane;
@@ -326,6 +361,13 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
                     if (i >= 3 * kLdsQ && h == 0) q = kKeepQ ? qf[kKeepQ ? s - kLdsQ : 0] : load_q(s);
                     f32x4& y = s % 2 ? odd[h] : sc[h];
                     y = mma16(x, q, y);
+                    if constexpr (kSpread) {              // load l behind product l kProducts / kLoads
+                        constexpr int kProducts = 2 * NS;
+                        static_assert(kLoads <= kProducts, "one a product");
+                        const int n = 2 * s + h, l = (n * kLoads + kProducts - 1) / kProducts;
+                        if (l < ((n + 1) * kLoads + kProducts - 1) / kProducts)
+                            load_of_tile<T, RC, WAVES>(l, next.whole, to, next.lo, next.hi, w, ln);
+                    }
                 }, [](int i) { return i >= 3 * kLdsQ || i % 3 != 0; });
             }
 #pragma unroll
@@ -391,7 +433,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
                 acc[0][i] = mma16(x, pf, acc[0][i]);
                 acc[1][i] = mma16(x, po, acc[1][i]);
             });
-            have = next;
+            have = next.have;
             wait_loads_and_lds();
             wg_barrier();
         }

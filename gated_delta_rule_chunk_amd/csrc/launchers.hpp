@@ -272,7 +272,6 @@ struct MlaStepArgs {
     unsigned int* status;       // counts keys in pages that do not exist
     int32_t n_pages, page_shift, max_pages, Nb, Tq, H, Dc, Dr;
     int32_t waves, groups, parts, join_rows;   // the split (mla_step_plan)
-    float part_cost;
     float scale;
     bool bf16;
 };

@@ -19,8 +19,7 @@
 // parts, one per workgroup. A workgroup walks through the sequences of its
 // part; a sequence that lies in one part is finished there, one that spans
 // several leaves (maximum, sum, output) of each part in the workspace, and a
-// second kernel joins them. Parts are long enough that a short cache does not
-// drown in partial results (part_tiles). Bound by the cache's bytes for many
+// second kernel joins them. Bound by the cache's bytes for many
 // rows of cache, by latency for few.
 #include "launchers.hpp"
 #include "mla_common.hpp"
@@ -139,12 +138,9 @@ __device__ __forceinline__ Scan scan_tiles(const MlaStepArgs& a, int b0, int lan
     }
     return x;
 }
-// Tiles a part: an even share, but no fewer than keeps the partial results
-// (a part's cost of writing and joining them against the time of a tile).
+// Tiles a part: an even share
 __device__ __forceinline__ int part_tiles(const MlaStepArgs& a, int total) {
-    const int per = (int)(((unsigned)total + (unsigned)a.parts - 1) / (unsigned)a.parts);
-    const int least = (int)__builtin_ceilf(__builtin_sqrtf((float)total) * a.part_cost);
-    const int x = per > least ? per : least;
+    const int x = (int)(((unsigned)total + (unsigned)a.parts - 1) / (unsigned)a.parts);
     return __builtin_amdgcn_readfirstlane(x > 1 ? x : 1);
 }
 
@@ -477,8 +473,43 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
 
 // Joins the parts of sequences that span several; writes zeros for sequences
 // without cache rows. A workgroup takes a.join_rows rows of queries of one
-// sequence, one after the other: its four waves take the parts in turn, each
-// over all columns, and their sums meet in LDS.
+// sequence. Up to kFewParts parts, each of its four waves takes rows of its own;
+// of more, they take the parts of a row in turn, and their sums meet in LDS.
+// Bound by latency: a row is two dependent reads.
+constexpr int kFewParts = 8;
+
+// A wave's part of a row of queries over parts p0 + at, + step, ...: the sums of
+// all columns, not yet divided by l.
+template <int DC>
+__device__ __forceinline__ void join_row(const MlaStepArgs& a, int row, int p0, int p1, int at, int step, int lane,
+                                         f32x4 (&s)[DC / 256], float& m, float& l) {
+    const int group = row / (16 * a.waves), r = row % (16 * a.waves);
+    m = -INFINITY;
+    for (int p = p0 + lane; p <= p1; p += 64) m = fmaxf(m, partial(a, group, p, p > p0 ? 0 : 1, r)[0]);
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
+    const float ms = m == -INFINITY ? 0.f : m;
+    l = 0.f;
+    for (int p = p0 + lane; p <= p1; p += 64) {
+        const float* x = partial(a, group, p, p > p0 ? 0 : 1, r);
+        l += x[1] * __builtin_amdgcn_exp2f(x[0] - ms);
+    }
+#pragma unroll
+    for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
+#pragma unroll
+    for (int v = 0; v < DC / 256; ++v) s[v] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll 8
+    for (int p = p0 + at; p <= p1; p += step) {
+        const float* x = partial(a, group, p, p > p0 ? 0 : 1, r);
+        const float f = __builtin_amdgcn_exp2f(x[0] - ms);
+#pragma unroll
+        for (int v = 0; v < DC / 256; ++v) {
+            const f32x4 y = *reinterpret_cast<const f32x4*>(x + 4 + 256 * v + 4 * lane);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) s[v][j] += f * y[j];
+        }
+    }
+}
 template <class T, int DC> __global__ __launch_bounds__(256) void mla_step_join_kernel(MlaStepArgs a, int blocks) {
     __shared__ __attribute__((aligned(16))) float sums[4][DC];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -493,53 +524,41 @@ template <class T, int DC> __global__ __launch_bounds__(256) void mla_step_join_
         }
         total += sq.all();
     }
-    T* op = static_cast<T*>(a.o) + ((int64_t)b * M + row0) * DC;
+    T* op = static_cast<T*>(a.o) + (int64_t)b * M * DC;
     float* lp = a.lse ? a.lse + (int64_t)b * M : nullptr;
     if (tiles == 0) {
-        for (int d = threadIdx.x; d < (row1 - row0) * DC; d += 256) op[d] = (T)0.f;
+        for (int d = threadIdx.x; d < (row1 - row0) * DC; d += 256) op[(int64_t)row0 * DC + d] = (T)0.f;
         if (lp)
             for (int i = row0 + threadIdx.x; i < row1; i += 256) lp[i] = -INFINITY;
         return;
     }
     const int per = part_tiles(a, total), p0 = first / per, p1 = (first + tiles - 1) / per;
     if (p0 == p1) return;
-    for (int row = row0; row < row1; ++row, op += DC) {
-        const int group = row / (16 * a.waves), r = row % (16 * a.waves);
-        float m = -INFINITY;
-        for (int p = p0 + lane; p <= p1; p += 64) m = fmaxf(m, partial(a, group, p, p > p0 ? 0 : 1, r)[0]);
+    f32x4 s[DC / 256];
+    float m, l;
+    auto inverse = [&] { return l > 0.f ? 1.f / l : l == 0.f ? 0.f : l; };
+    auto put_lse = [&](int row) {
+        if (lp) lp[row] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+    };
+    if (p1 - p0 < kFewParts) {
+        for (int row = row0 + w; row < row1; row += 4) {
+            join_row<DC>(a, row, p0, p1, 0, 1, lane, s, m, l);
+            const float inv = inverse();
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
-        const float ms = m == -INFINITY ? 0.f : m;
-        float l = 0.f;
-        for (int p = p0 + lane; p <= p1; p += 64) {
-            const float* x = partial(a, group, p, p > p0 ? 0 : 1, r);
-            l += x[1] * __builtin_amdgcn_exp2f(x[0] - ms);
+            for (int v = 0; v < DC / 256; ++v) store4(op + (int64_t)row * DC + 256 * v + 4 * lane, s[v], inv);
+            if (lane == 0) put_lse(row);
         }
+        return;
+    }
+    for (int row = row0; row < row1; ++row) {
+        join_row<DC>(a, row, p0, p1, w, 4, lane, s, m, l);
 #pragma unroll
-        for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
-        constexpr int V = DC / 256;
-        f32x4 s[V];
-#pragma unroll
-        for (int v = 0; v < V; ++v) s[v] = f32x4{0.f, 0.f, 0.f, 0.f};
-#pragma unroll 4
-        for (int p = p0 + w; p <= p1; p += 4) {
-            const float* x = partial(a, group, p, p > p0 ? 0 : 1, r);
-            const float f = __builtin_amdgcn_exp2f(x[0] - ms);
-#pragma unroll
-            for (int v = 0; v < V; ++v) {
-                const f32x4 y = *reinterpret_cast<const f32x4*>(x + 4 + 256 * v + 4 * lane);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) s[v][j] += f * y[j];
-            }
-        }
-#pragma unroll
-        for (int v = 0; v < V; ++v) *reinterpret_cast<f32x4*>(&sums[w][256 * v + 4 * lane]) = s[v];
+        for (int v = 0; v < DC / 256; ++v) *reinterpret_cast<f32x4*>(&sums[w][256 * v + 4 * lane]) = s[v];
         __syncthreads();
-        const float inv = l > 0.f ? 1.f / l : l == 0.f ? 0.f : l;
+        const float inv = inverse();
         for (int d = threadIdx.x; d < DC; d += 256)
-            op[d] = (T)((((sums[0][d] + sums[1][d]) + sums[2][d]) + sums[3][d]) * inv);
-        if (lp && threadIdx.x == 0)
-            lp[row] = l == 0.f ? -INFINITY : (m + __builtin_amdgcn_logf(l)) * 0.6931471805599453f;
+            op[(int64_t)row * DC + d] = (T)((((sums[0][d] + sums[1][d]) + sums[2][d]) + sums[3][d]) * inv);
+        if (threadIdx.x == 0) put_lse(row);
         __syncthreads();
     }
 }
@@ -614,9 +633,6 @@ size_t mla_step_plan(MlaStepArgs& a) {
     if (parts < 32) parts = 32;
     if (parts > most) parts = most;
     a.parts = (int32_t)(parts > 1 ? parts : 1);
-    // writing and joining a part's results, in tiles: about 1/16 a tile for 96
-    // rows of 512 columns; the sum of both costs is least at sqrt(total) / 4
-    a.part_cost = 0.25f;
     // the join: about 1024 workgroups, most of which find nothing to join
     const int64_t j = (a.Nb * rows + 1023) / 1024;
     a.join_rows = (int32_t)(j < rows ? j : rows);

@@ -270,19 +270,30 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
         // 16 rows, in an even one and the next: of the same 64.
         const int32_t* table = a.table + (int64_t)b * a.max_pages;
         int pbase = -64, pages = 0;
+        auto entry = [&](int p) {
+            const int i = p + lane;
+            return i < a.max_pages && (int64_t)i << ps < len ? table[i] : 0;
+        };
+        auto keep = [&](int p, int e) {
+            pbase = p;
+            const int64_t r = (int64_t)(p + lane) << ps;
+            if (e < 0 || e >= a.n_pages) e = -1;
+            // counted once: where the page's first row is this part's
+            const uint64_t bad = __ballot(e < 0 && r >= t0 * kTile && r < (int64_t)t1 * kTile);
+            if (bad && group == 0 && w == 0 && lane == 0) atomicAdd(a.status, (unsigned)__popcll(bad));
+            pages = r < len ? e : -1;
+        };
+        // the first entries and the queries are under way together
+        const int p0 = t0 * kTile >> ps, e = entry(p0);
+        Frag<T> qf[kKeepQ ? NS : 1];
+        if constexpr (kKeepQ) {
+#pragma unroll
+            for (int s = 0; s < NS; ++s) qf[s] = load_q(s);
+        }
+        keep(p0, e);
         auto find = [&](int t) {
             const int k0 = t * kTile, p = k0 >> ps;
-            if (p >= pbase + 64) {
-                pbase = p;
-                const int i = p + lane;
-                const int64_t r = (int64_t)i << ps;
-                int e = i < a.max_pages && r < len ? table[i] : 0;
-                if (e < 0 || e >= a.n_pages) e = -1;
-                // counted once: where the page's first row is this part's
-                const uint64_t bad = __ballot(e < 0 && r >= t0 * kTile && r < (int64_t)t1 * kTile);
-                if (bad && group == 0 && w == 0 && lane == 0) atomicAdd(a.status, (unsigned)__popcll(bad));
-                pages = r < len ? e : -1;
-            }
+            if (p >= pbase + 64) keep(p, entry(p));
             const int e0 = __builtin_amdgcn_readlane(pages, p - pbase);
             const int e1 = __builtin_amdgcn_readlane(pages, ((k0 + 16) >> ps) - pbase);
             const int mask = (1 << ps) - 1;
@@ -309,12 +320,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
         if (next.whole) load_whole(next, smem[0]);
         else load_edge(next, t0, smem[0]);
         int have = next.have;
-        Frag<T> qf[kKeepQ ? NS - kLdsQ : 1];
         if constexpr (kKeepQ) {
 #pragma unroll
-            for (int s = 0; s < kLdsQ; ++s) lds_q[w][s][lane] = load_q(s);
-#pragma unroll
-            for (int s = kLdsQ; s < NS; ++s) qf[s - kLdsQ] = load_q(s);
+            for (int s = 0; s < kLdsQ; ++s) lds_q[w][s][lane] = qf[s];
         }
         wait_loads_and_lds();
         wg_barrier();
@@ -354,7 +362,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
                     }
                     const int s = i < 3 * kLdsQ ? i / 3 : (i - kLdsQ) / 2;
                     const int h = i < 3 * kLdsQ ? i % 3 - 1 : (i - kLdsQ) % 2;
-                    if (i >= 3 * kLdsQ && h == 0) q = kKeepQ ? qf[kKeepQ ? s - kLdsQ : 0] : load_q(s);
+                    if (i >= 3 * kLdsQ && h == 0) q = kKeepQ ? qf[kKeepQ ? s : 0] : load_q(s);
                     f32x4& y = s % 2 ? odd[h] : sc[h];
                     y = mma16(x, q, y);
                     if constexpr (kSpread) {              // load l behind product l kProducts / kLoads
@@ -622,13 +630,17 @@ template <class T> hipError_t launch_dims(const MlaStepArgs& a, hipStream_t s) {
 }  // namespace
 
 // The split over workgroups. The blocks of 32 rows of queries are spread evenly
-// over as few groups as hold them, two waves a block.
+// over as few groups as hold them, two waves a block: every group reads the
+// cache. A cache so short that there is a compute unit for each tile and group
+// gets more of them, as time is then what one tile and its results take.
 size_t mla_step_plan(MlaStepArgs& a) {
     const int64_t rows = (int64_t)a.Tq * a.H, blocks = (rows + 31) / 32;
-    const int most_blocks = (!a.bf16 && a.Dc == 512 ? max_waves<float, 512>() : 8) / 2;
-    a.groups = (int32_t)((blocks + most_blocks - 1) / most_blocks);
-    a.waves = (int32_t)((blocks + a.groups - 1) / a.groups) * 2;
     const int64_t most = (int64_t)a.Nb * ((((int64_t)a.max_pages << a.page_shift) + kTile - 1) / kTile);
+    const int most_blocks = (!a.bf16 && a.Dc == 512 ? max_waves<float, 512>() : 8) / 2;
+    int64_t per = most_blocks;                                    // blocks a workgroup
+    while (per > 1 && (blocks + per - 2) / (per - 1) * most <= 256) --per;
+    a.groups = (int32_t)((blocks + per - 1) / per);
+    a.waves = (int32_t)((blocks + a.groups - 1) / a.groups) * 2;
     int64_t parts = 256 / a.groups;
     if (parts < 32) parts = 32;
     if (parts > most) parts = most;

@@ -164,7 +164,8 @@ def _ptr(t):
 
 
 def _stream(device):
-    return ctypes.c_void_p(torch.cuda.current_stream(device).cuda_stream)
+    # the handle itself: a Stream object around it costs 2 us a call
+    return ctypes.c_void_p(torch._C._cuda_getCurrentRawStream(device.index))
 
 
 def _need(t, name, shape, dtype, device):
@@ -857,7 +858,10 @@ def _workspace(workspace, need, dev):
 
 def _steps(t, *dims):
     """Strides of dimensions (0 along those of one element, where any value serves)."""
-    return [0 if t is None or t.shape[d] == 1 else t.stride(d) for d in dims]
+    if t is None:
+        return [0] * len(dims)
+    shape, stride = t.shape, t.stride()
+    return [0 if shape[d] == 1 else stride[d] for d in dims]
 
 
 def _mla_inputs(q, kv, k_rope, cu_seqlens_q, cu_seqlens_k, scale):
@@ -1061,7 +1065,7 @@ def device_check(device=None):
     dev = torch.device("cuda", torch.cuda.current_device()) if device is None else torch.device(device)
     lib = load_library()
     with torch.cuda.device(dev):
-        _check(lib.kda_device_check(_stream(dev)))
+        _check(lib.kda_device_check(ctypes.c_void_p(torch.cuda.current_stream(dev).cuda_stream)))
 
 
 def set_wait_limit(polls: int):

@@ -203,7 +203,7 @@ template <class T> __global__ __launch_bounds__(256) void mla_dkr_kernel(MlaArgs
 template <class T, int DN, int DR> hipError_t launch_dq(const MlaArgs& a, hipStream_t s) {
     if (a.Tq == 0) return hipSuccess;
     int64_t slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 128);
-    if (slots * a.H < kSmallLaunch) {
+    if (slots * a.H < kSmallLaunch<T>) {
         slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 32);
         mla_dq_kernel<T, DN, DR, true><<<dim3((unsigned)(slots * a.H)), 256, 0, s>>>(a, slots);
     } else {

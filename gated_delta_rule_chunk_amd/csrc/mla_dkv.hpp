@@ -206,7 +206,7 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
 template <class T, int DN, int DR> hipError_t launch_dkv(const MlaArgs& a, hipStream_t s) {
     if (a.Tk == 0) return hipSuccess;
     int64_t slots = tile_slots(a.cuk, a.B, a.N, a.Tk, 128);
-    if (slots * a.H < kSmallLaunch) {
+    if (slots * a.H < kSmallLaunch<T>) {
         slots = tile_slots(a.cuk, a.B, a.N, a.Tk, 32);
         mla_dkv_kernel<T, DN, DR, true><<<dim3((unsigned)(slots * a.H)), 256, 0, s>>>(a, slots);
     } else {

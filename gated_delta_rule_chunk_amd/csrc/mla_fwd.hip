@@ -210,7 +210,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_fwd_kernel(Ml
 
 template <class T, int DN, int DR> hipError_t launch(const MlaArgs& a, hipStream_t s) {
     int64_t slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 128);
-    if (slots * a.H < kSmallLaunch) {
+    if (slots * a.H < kSmallLaunch<T>) {
         slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 32);
         mla_fwd_kernel<T, DN, DR, true><<<dim3((unsigned)(slots * a.H)), 256, 0, s>>>(a, slots);
     } else {

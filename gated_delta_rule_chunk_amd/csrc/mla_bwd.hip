@@ -12,7 +12,14 @@
 // adding dq from the second kernel's workgroups instead would take an atomic
 // per query row, key tile and column, more bytes than the scores cost
 // products. A third kernel sums the shared part over the heads, in their
-// order, from float32 shares. Bound by the matrix cores.
+// order, from float32 shares. Bound by the matrix cores; measured, bf16,
+// causal, 4096 tokens, 96 heads of 128 + 64 channels: 745-790 us for dq (512
+// products a score and head: 1050-1110 TFLOP/s), 1170-1330 us for dk and dv (640:
+// 780-880 TFLOP/s), 18 us for the sum over the heads (100 MB read, 5.6 TB/s).
+// Rounding: bf16 operands are rounded once, p and ds among them; D comes from
+// o as the forward returned it. An independent error of up to 2^-9 of each ds
+// leaves dq with about the error that its own rounding has (0.0017 of its
+// norm), 0.0025 together.
 #include "launchers.hpp"
 #include "mla_common.hpp"
 #include "mla_dkv.hpp"

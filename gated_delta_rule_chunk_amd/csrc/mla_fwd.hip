@@ -9,7 +9,11 @@
 // global memory to LDS, two buffers, the next tile in flight while one is
 // computed; queries, scores, probabilities and outputs stay in registers (the
 // scores are formed transposed: mla_common.hpp). Bound by the matrix cores and
-// the exponentials: 2 (2 Dn + Dr) products per score.
+// the exponentials, 2 (2 Dn + Dr) products per score: a wave's own matrix and
+// vector instructions hardly overlap, those of the two waves on a SIMD do.
+// Measured, bf16, causal, 4096 tokens, 96 heads of 128 + 64 channels: 540-565
+// us, 920-950 TFLOP/s over the visible pairs (a plain 8192^3 product of the
+// library: 1131), matrix cores busy 55% of the time, no bank conflicts.
 #include "launchers.hpp"
 #include "mla_common.hpp"
 

@@ -19,8 +19,15 @@
 // parts, one per workgroup. A workgroup walks through the sequences of its
 // part; a sequence that lies in one part is finished there, one that spans
 // several leaves (maximum, sum, output) of each part in the workspace, and a
-// second kernel joins them. Bound by the cache's bytes for many
-// rows of cache, by latency for few.
+// second kernel joins them.
+//
+// Measured, bf16, 96 heads, Dc = 512, Dr = 64. 128 sequences of 4096 to 8192
+// rows (922 MB): 237-280 us and 20 us for the join, 3.3-3.9 TB/s; the cache's tiles
+// alone load in 187 us. A tile takes 4600 clocks: SIMDs 0 and 1 hold two of the
+// six waves (2200 clocks of matrix instructions), LDS delivers for 1500, and at
+// the clock that this load leaves, 1.9-2.2 GHz, that is the time. One sequence of
+// 100001 rows (115 MB): 42 us, of which 28 are its 13 tiles a workgroup, and 14
+// us for the join of 256 parts (47 MB). One of 1000 rows: 11 and 5 us, latency.
 #include "launchers.hpp"
 #include "mla_common.hpp"
 
@@ -483,7 +490,9 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
 // without cache rows. A workgroup takes a.join_rows rows of queries of one
 // sequence. Up to kFewParts parts, each of its four waves takes rows of its own;
 // of more, they take the parts of a row in turn, and their sums meet in LDS.
-// Bound by latency: a row is two dependent reads.
+// Bound by latency: a row is two dependent reads. Rows of a wave's own against
+// shared ones: 3 parts (128 sequences, 96 heads) 20 against 39 us; 16 parts of
+// one sequence 5.1 against 4.1 us.
 constexpr int kFewParts = 8;
 
 // A wave's part of a row of queries over parts p0 + at, + step, ...: the sums of
@@ -571,7 +580,9 @@ template <class T, int DC> __global__ __launch_bounds__(256) void mla_step_join_
     }
 }
 
-// One thread per 16-byte chunk of a new token.
+// One thread per 16-byte chunk of a new token. Bound by HBM, few tokens by the
+// launch: 28000 tokens of 1152 bytes (65 MB read and written) 14-15.7 us, 4.1-4.6
+// TB/s (a plain copy: 4.8); 128 tokens 3 us.
 template <class T> __global__ __launch_bounds__(256) void mla_append_kernel(MlaAppendArgs a, int64_t chunks) {
     const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
     if (x >= chunks) return;
@@ -632,7 +643,9 @@ template <class T> hipError_t launch_dims(const MlaStepArgs& a, hipStream_t s) {
 // The split over workgroups. The blocks of 32 rows of queries are spread evenly
 // over as few groups as hold them, two waves a block: every group reads the
 // cache. A cache so short that there is a compute unit for each tile and group
-// gets more of them, as time is then what one tile and its results take.
+// gets more of them, as time is then what one tile and its results take (32
+// tiles, 96 heads: 11.2 us in three groups, 14.9 in one; a cache of 3126 tiles
+// would be read three times).
 size_t mla_step_plan(MlaStepArgs& a) {
     const int64_t rows = (int64_t)a.Tq * a.H, blocks = (rows + 31) / 32;
     const int64_t most = (int64_t)a.Nb * ((((int64_t)a.max_pages << a.page_shift) + kTile - 1) / kTile);

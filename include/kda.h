@@ -636,13 +636,14 @@ kda_status kda_recurrent_step_conv(const void* xq, const void* xk, const void* x
  * each give-up in a per-device status word, finishes normally, and
  * kda_device_check reports it: failures are explicit (ISEEKYAN/k3 README,
  * package scope). A second status word counts log-decays out of the range
- * the matrix-core kernels need (see the conventions above).
+ * the matrix-core kernels need (see the conventions above), a third one rows
+ * whose cache page does not exist (kda_mla.h).
  *
  * kda_device_check waits for the work enqueued on `stream`, then returns
  * KDA_OK if, since the previous check (or since the library was loaded), no
- * bounded wait of any call on the current device gave up and no gate fell
- * outside its range, and KDA_ERR_DEVICE otherwise (kda_last_error_message
- * says which, with the count). The check itself synchronises, so it belongs
+ * bounded wait of any call on the current device gave up, no gate fell
+ * outside its range and no cache page was missing, and KDA_ERR_DEVICE
+ * otherwise (kda_last_error_message says which, with the count). The check itself synchronises, so it belongs
  * outside timed or captured regions.
  */
 kda_status kda_device_check(void* stream);

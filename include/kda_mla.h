@@ -16,14 +16,18 @@
  * keys into the query and the output, and the queries meet the cached latents
  * themselves; for generated tokens. The projections are outside the library.
  *
- * A row that sees no key has o = 0 and lse = -inf. A NaN or an infinity in a
- * row of k, r or the cache reaches only rows that see it; in a row of v it may
- * reach every row of its sequence (a hidden key's weight is an exact 0, and
- * 0 * NaN is NaN). Cache rows past a sequence's length are never read.
+ * A row that sees no key has o = 0 and lse = -inf. Forward: a NaN or an infinity
+ * in a row of k or r reaches only rows that see it; in a row of v, and in the
+ * latent part of a cache row, which is both, it may reach every row of its
+ * sequence (a hidden key's weight is an exact 0, and 0 * NaN is NaN). Backward:
+ * it may reach every gradient of its sequence. Other sequences are not
+ * touched. Cache rows past a sequence's length are never read.
  *
  * dtype: KDA_BF16 runs on the bf16 matrix cores, scores, softmax statistics
  * and sums in float32, probabilities and score gradients rounded to bf16 once
- * as operands of the second product. KDA_F32 runs on the float32 matrix cores.
+ * as operands of the second product (relative to the norm of the result, an
+ * error of about 0.0017 each, next to the 0.0017 of the result's own rounding).
+ * KDA_F32 runs on the float32 matrix cores.
  *
  * Preconditions that are not checked: finite inputs; cu_seqlens starting at 0
  * and non-decreasing. Offsets are clipped to the tensor, so that a wrong one
@@ -60,7 +64,8 @@ extern "C" {
  *   zero_rest  see above (packed calls only; ignored otherwise)
  *   o       [B,Tq,H,Dn] dtype;  lse [B,H,Tq] float32, or NULL
  * Neither may alias an input. Every tensor pointer is 16-byte aligned.
- * Supported: Dn in {64, 128}, Dr in {0, 64}, KDA_BF16 and KDA_F32.
+ * Supported: Dn in {64, 128}, Dr in {0, 64}, KDA_BF16 and KDA_F32, H <= 4096,
+ * k_rope_row <= 2^22; sizes past what the offsets hold are refused.
  * Tq = 0 is a no-op; with Tk = 0, kv and k_rope may be NULL.
  */
 kda_status kda_mla_fwd(const void* q, const void* kv, const void* k_rope, int64_t k_rope_row, int64_t k_rope_batch,
@@ -93,8 +98,9 @@ kda_status kda_mla_bwd(const void* q, const void* kv, const void* k_rope, int64_
  * shared key part), [n_pages,page_size,Dc+Dr] dtype, 16-byte aligned. Row p of
  * sequence n lies in page page_table[n][p / page_size] at p % page_size;
  * page_table is [Nb,max_pages] int32, entries past a sequence's length are not
- * read. page_size is a power of two, 16 or more. Pages may be shared by
- * sequences (a common prefix) as long as nobody writes to them.
+ * read. page_size is a power of two, 16 to 2^24; max_pages * page_size is at
+ * most 2^30. Pages may be shared by sequences (a common prefix) as long as
+ * nobody writes to them.
  *
  * A page_table entry outside [0, n_pages) for a row within the length, or a
  * length past max_pages * page_size, is a fault of the caller that only the

@@ -266,6 +266,53 @@ def test_step_split_over_the_cache(dtype, lens):
     assert torch.equal(o, again[0]) and torch.equal(lse, again[1])
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Dc,Dr", [(512, 64), (512, 0), (256, 64), (256, 0)])
+@pytest.mark.parametrize("H", [64, 96, 128])
+def test_step_wide_workgroups(dtype, Dc, Dr, H):
+    """A cache long enough that all rows of queries that fit share a workgroup: four, six and eight waves."""
+    lens = [2900, 31, 1000]
+    cache, table, rows = _cache(lens, 64, Dc, Dr, dtype, H)
+    ql, qr = _queries(3, 1, H, Dc, Dr, dtype, 3)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = kda.mla_step(ql, qr, cache, table, n, scale=0.06)
+    _check_step(ql, qr, rows, o, lse, 0.06, lens)
+
+
+@pytest.mark.parametrize("H,tiles", [(4, 8), (4, 9), (96, 8), (96, 9)])
+def test_step_few_and_many_parts(H, tiles):
+    """Sequences of one tile a part: joined by a wave each up to eight parts, by four together beyond."""
+    lens = [32 * tiles, 32 * tiles - 31]
+    cache, table, rows = _cache(lens, 32, 512, 64, BF16, tiles)
+    ql, qr = _queries(2, 1, H, 512, 64, BF16, 8)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = kda.mla_step(ql, qr, cache, table, n, scale=0.07)
+    _check_step(ql, qr, rows, o, lse, 0.07, lens)
+
+
+def test_step_parts_of_more_pages_than_lanes():
+    """Parts of over 64 pages of 16 rows read the page table in pieces; a page that does not exist in any
+    of them is hidden and counted once."""
+    lens = [6500 + 41 * i for i in range(40)]
+    cache, table, rows = _cache(lens, 16, 256, 64, BF16, 20)
+    assert sum(-(-n // 32) for n in lens) > 256 * 32
+    ql, qr = _queries(len(lens), 1, 3, 256, 64, BF16, 21)
+    n = torch.tensor(lens, dtype=torch.int32, device="cuda")
+    o, lse = kda.mla_step(ql, qr, cache, table, n, scale=0.08)
+    _check_step(ql, qr, rows, o, lse, 0.08, lens)
+    bad = table.clone()
+    bad[::2, 63], bad[1::2, 64], bad[:, 300] = -1, cache.shape[0], -7
+    o, lse = kda.mla_step(ql, qr, cache, bad, n, scale=0.08)
+    with pytest.raises(kda.KDAError, match="80 counted"):
+        kda.device_check()
+    hidden = torch.zeros(max(lens), dtype=torch.bool, device="cuda")
+    hidden[4800:4816] = True
+    for b, x in enumerate(rows):
+        gone = hidden[:lens[b]].clone()
+        gone[(63 + b % 2) * 16:(64 + b % 2) * 16] = True
+        _check_step(ql[b:b + 1], qr[b:b + 1], [x[~gone]], o[b:b + 1], lse[b:b + 1], 0.08, [int((~gone).sum())])
+
+
 def test_step_large_scores():
     lens = [900]
     cache, table, rows = _cache(lens, 64, 512, 64, BF16, 14)

@@ -11,8 +11,8 @@
 // scores are formed transposed: mla_common.hpp). Bound by the matrix cores and
 // the exponentials, 2 (2 Dn + Dr) products per score: a wave's own matrix and
 // vector instructions hardly overlap, those of the two waves on a SIMD do.
-// Measured, bf16, causal, 4096 tokens, 96 heads of 128 + 64 channels: 540-565
-// us, 920-950 TFLOP/s over the visible pairs (a plain 8192^3 product of the
+// Measured, bf16, causal, 4096 tokens, 96 heads of 128 + 64 channels: 505-565
+// us, 910-1020 TFLOP/s over the visible pairs (a plain 8192^3 product of the
 // library: 1131), matrix cores busy 55% of the time, no bank conflicts.
 #include "launchers.hpp"
 #include "mla_common.hpp"

@@ -213,10 +213,12 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
     constexpr int D = DC + DR, RC = D / kChunk<T>, kBuf = kTile * RC * 16;
     constexpr int NS = D / 32, ND = DC / 32;          // steps of the scores, blocks of the output's half
     // Not all queries fit the registers beside an output of 512 columns and what
-    // is under way: the first kLdsQ steps' of bf16 stay in LDS, and float32's
-    // are read again for every tile (its products take 16 times as long).
-    constexpr bool kKeepQ = sizeof(T) == 2;
-    constexpr int kLdsQ = kKeepQ && DC == 512 ? 8 : 0;
+    // is under way: the first kLdsQ steps' of bf16 stay in LDS. float32's stay in
+    // registers where they fit beside the output or with one wave per SIMD;
+    // otherwise they are read again for every tile (64 sequences of 4096 rows, 64
+    // heads: kept 208, read again 271 us for Dc = 256, 361 and 521 for 512).
+    constexpr bool kKeepQ = sizeof(T) == 2 || DC == 256 || WAVES <= 4;
+    constexpr int kLdsQ = sizeof(T) == 2 && DC == 512 ? 8 : 0;
     // bf16: the next tile's loads go out one by one under the products of the
     // scores. All at once, a wave waits about 150 clocks for each. float32's
     // products leave no registers for them, and take far longer than the loads.

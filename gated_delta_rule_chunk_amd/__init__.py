@@ -171,7 +171,7 @@ def _stream(device):
 def _need(t, name, shape, dtype, device):
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -830,7 +830,7 @@ def _need_rows(t, name, shape, dtype, device):
     dimensions are strided (the library checks the strides' alignment)."""
     if not isinstance(t, torch.Tensor):
         raise TypeError(f"{name} must be a torch.Tensor")
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape and tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name} has shape {tuple(t.shape)}, expected {tuple(shape)}")
     if t.dtype != dtype:
         raise TypeError(f"{name} has dtype {t.dtype}, expected {dtype}")
@@ -845,7 +845,7 @@ _HERE_ALREADY = contextlib.nullcontext()
 
 def _on(dev):
     """Makes dev the current device for a launch, where it is not already."""
-    return _HERE_ALREADY if dev.index == torch.cuda.current_device() else torch.cuda.device(dev)
+    return _HERE_ALREADY if dev.index == torch._C._cuda_getDevice() else torch.cuda.device(dev)
 
 
 def _workspace(workspace, need, dev):

@@ -496,6 +496,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
 // shared ones: 3 parts (128 sequences, 96 heads) 20 against 39 us; 16 parts of
 // one sequence 5.1 against 4.1 us.
 constexpr int kFewParts = 8;
+constexpr int kMaxParts = 256;  // mla_step_plan makes no more
 
 // A wave's part of a row of queries over parts p0 + at, + step, ...: the sums of
 // all columns, not yet divided by l.
@@ -503,16 +504,27 @@ template <int DC>
 __device__ __forceinline__ void join_row(const MlaStepArgs& a, int row, int p0, int p1, int at, int step, int lane,
                                          f32x4 (&s)[DC / 256], float& m, float& l) {
     const int group = row / (16 * a.waves), r = row % (16 * a.waves);
-    m = -INFINITY;
-    for (int p = p0 + lane; p <= p1; p += 64) m = fmaxf(m, partial(a, group, p, p > p0 ? 0 : 1, r)[0]);
+    float pm[kMaxParts / 64], pl[kMaxParts / 64];        // all under way together
+#pragma unroll
+    for (int k = 0; k < kMaxParts / 64; ++k) {
+        const int p = p0 + 64 * k + lane;
+        pm[k] = -INFINITY;
+        pl[k] = 0.f;
+        if (p <= p1) {
+            const float* x = partial(a, group, p, p > p0 ? 0 : 1, r);
+            pm[k] = x[0];
+            pl[k] = x[1];
+        }
+    }
+    m = pm[0];
+#pragma unroll
+    for (int k = 1; k < kMaxParts / 64; ++k) m = fmaxf(m, pm[k]);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
     const float ms = m == -INFINITY ? 0.f : m;
     l = 0.f;
-    for (int p = p0 + lane; p <= p1; p += 64) {
-        const float* x = partial(a, group, p, p > p0 ? 0 : 1, r);
-        l += x[1] * __builtin_amdgcn_exp2f(x[0] - ms);
-    }
+#pragma unroll
+    for (int k = 0; k < kMaxParts / 64; ++k) l += pl[k] * __builtin_amdgcn_exp2f(pm[k] - ms);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
 #pragma unroll
@@ -656,7 +668,7 @@ size_t mla_step_plan(MlaStepArgs& a) {
     while (per > 1 && (blocks + per - 2) / (per - 1) * most <= 256) --per;
     a.groups = (int32_t)((blocks + per - 1) / per);
     a.waves = (int32_t)((blocks + a.groups - 1) / a.groups) * 2;
-    int64_t parts = 256 / a.groups;
+    int64_t parts = kMaxParts / a.groups;
     if (parts < 32) parts = 32;
     if (parts > most) parts = most;
     a.parts = (int32_t)(parts > 1 ? parts : 1);

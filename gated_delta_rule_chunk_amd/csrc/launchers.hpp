@@ -253,8 +253,14 @@ struct MlaArgs {
     void* dkv;
     void* dkr;                  // [B,Tk,Dr] contiguous, nullptr when Dr = 0
     float* delta;               // workspace [B,H,Tq]: sum of d_o * o over a row
-    float* dkr_part;            // workspace [H,B,Tk,Dr]: per-head gradients of the shared key part
+    float* dkr_part;            // workspace [k_parts,H,B,Tk,Dr]: per-head gradients of the shared key part
+    // split kernels: workgroups that share a block of queries (keys), each with
+    // a float32 result of its own: workspace [q_parts,B,Tq,H,Dn+Dr], [k_parts,B,Tk,H,2*Dn]
+    int32_t q_parts, k_parts;
+    float* dq_part;
+    float* dkv_part;
 };
+size_t mla_bwd_plan(MlaArgs& a);   // sets the parts; bytes of the workspace
 
 // Absorbed form over a paged cache of latents (kda_mla_step), and its write
 // (kda_mla_cache_append).

@@ -16,7 +16,6 @@ kda_status fail(kda_status st, const char* fmt, ...) {
 }
 
 bool aligned(const void* p) { return ((uintptr_t)p & 15) == 0; }
-size_t up16(size_t n) { return (n + 15) / 16 * 16; }
 
 struct Ranges {     // inputs and outputs that may not be the same memory
     const char* fn;
@@ -137,7 +136,11 @@ kda_status kda_mla_fwd(const void* q, const void* kv, const void* k_rope, int64_
 
 size_t kda_mla_bwd_workspace_bytes(int32_t B, int32_t Tq, int32_t Tk, int32_t H, int32_t Dr) {
     if (B < 1 || Tq < 0 || Tk < 0 || H < 1 || (Dr != 0 && Dr != 64)) return 0;
-    return up16((size_t)B * H * Tq * sizeof(float)) + (size_t)H * B * Tk * Dr * sizeof(float);
+    // enough for any call: packed sequences have no fewer tiles and bf16 no more
+    // parts than dense float32 ones
+    kda::MlaArgs a{};
+    a.B = B; a.Tq = Tq; a.Tk = Tk; a.H = H; a.Dn = 128; a.Dr = Dr; a.N = B;
+    return kda::mla_bwd_plan(a);
 }
 
 kda_status kda_mla_bwd(const void* q, const void* kv, const void* k_rope, int64_t k_rope_row, int64_t k_rope_batch,
@@ -180,7 +183,7 @@ kda_status kda_mla_bwd(const void* q, const void* kv, const void* k_rope, int64_
     a.lse = const_cast<float*>(lse);
     a.d_o = d_o; a.dq = dq; a.dkv = dkv; a.dkr = dk_rope;
     a.delta = static_cast<float*>(workspace);
-    a.dkr_part = reinterpret_cast<float*>(static_cast<char*>(workspace) + up16((size_t)B * H * Tq * sizeof(float)));
+    kda::mla_bwd_plan(a);
     return finish(fn, kda::launch_mla_bwd(a, static_cast<hipStream_t>(stream)));
 }
 

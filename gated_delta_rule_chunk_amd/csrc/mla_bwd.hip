@@ -12,7 +12,8 @@
 // adding dq from the second kernel's workgroups instead would take an atomic
 // per query row, key tile and column, more bytes than the scores cost
 // products. A third kernel sums the shared part over the heads, in their
-// order, from float32 shares. Bound by the matrix cores; measured, bf16,
+// order, from float32 shares; in launches of few workgroups several of them
+// share a block, and it sums their results too. Bound by the matrix cores; measured, bf16,
 // causal, 4096 tokens, 96 heads of 128 + 64 channels: 745-790 us for dq (512
 // products a score and head: 1050-1110 TFLOP/s), 1170-1330 us for dk and dv (640:
 // 780-880 TFLOP/s), 18 us for the sum over the heads (100 MB read, 5.6 TB/s).
@@ -41,7 +42,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_
     const int n32 = lane & 31, hf = lane >> 5, lw = SPLIT ? 0 : w;
     int h;
     int64_t slot;
-    head_and_slot(slots, a.H, h, slot);
+    const int part = SPLIT ? (int)(blockIdx.x / (slots * a.H)) : 0;
+    head_and_slot(blockIdx.x - part * slots * a.H, slots, a.H, h, slot);
     int n, q0, Lq, Lk;
     int64_t qs, ks;
     if (!tile_of(a.cuq, a.N, a.Tq, BM, slots - 1 - slot, lane, n, qs, Lq, q0)) return;
@@ -83,7 +85,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_
             for (int j = 0; j < 8; ++j) delta += (float)df[s][j] * (float)of[j];
         }
         delta = half_sum(delta);
-        if (live && hf == 0 && !rest && w == (SPLIT ? 0 : w)) a.delta[srow] = delta;
+        if (live && hf == 0 && !rest && part == 0 && w == (SPLIT ? 0 : w)) a.delta[srow] = delta;
     }
     f32x16 acc[DQ / 32];
 #pragma unroll
@@ -154,7 +156,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_
     };
     T* p = static_cast<T*>(a.dq) + qrow * DQ;
     if constexpr (SPLIT) {
-        for (int t = w; t < tiles; t += 4) {
+        for (int t = w + 4 * part; t < tiles; t += 4 * a.q_parts) {
             load(t, smem[w]);
             wait_loads_and_lds();
             compute(t, smem[w]);
@@ -165,8 +167,12 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_
         wait_loads_and_lds();
         wg_barrier();
         const float one[4] = {1.f, 1.f, 1.f, 1.f};
-        for (int d = w; d < DQ / 32; d += 4)
-            store_tile<T>(p + 32 * d, sum_blocks(smem[0], kBuf, d, one, lane), a.scale, hf, live);
+        float* f = a.q_parts > 1 ? a.dq_part + (((int64_t)part * a.B * a.Tq * a.H) + qrow) * DQ : nullptr;
+        for (int d = w; d < DQ / 32; d += 4) {
+            const f32x16 x = sum_blocks(smem[0], kBuf, d, one, lane);
+            if (f) store_tile<float>(f + 32 * d, x, a.scale, hf, live);
+            else store_tile<T>(p + 32 * d, x, a.scale, hf, live);
+        }
     } else {
         if (tiles > 0) load(0, smem[0]);
         wait_loads_and_lds();
@@ -182,27 +188,42 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_
     }
 }
 
-// Sums the shared key part's shares over the heads, in their order: four
-// columns a thread.
-template <class T> __global__ __launch_bounds__(256) void mla_dkr_kernel(MlaArgs a, int64_t quads) {
-    const int64_t x = (int64_t)blockIdx.x * 256 + threadIdx.x;
-    if (x >= quads) return;
-    const int64_t per = (int64_t)a.B * a.Tk * a.Dr;
-    if (a.cuk && !a.zero_rest) {
+// The float32 shares of a gradient (the heads' of the shared key part; those of
+// workgroups that shared a block) summed in their order: up to three gradients
+// a launch, four columns a thread.
+struct Shares {
+    const float* in;            // [n] of quads * 4
+    void* out;
+    int32_t n, row_quads, T;
+    const int32_t* cu;          // packed: rows behind the last sequence are left alone, unless they are zeroed
+    int64_t quads;
+    int64_t blocks;             // workgroups of this one and of those before it
+};
+struct SharesArgs {
+    Shares of[3];
+    int32_t N;
+    bool zero_rest;
+};
+template <class T> __global__ __launch_bounds__(256) void mla_sum_kernel(SharesArgs a) {
+    const int which = (int)blockIdx.x < a.of[0].blocks ? 0 : (int)blockIdx.x < a.of[1].blocks ? 1 : 2;
+    const Shares& g = a.of[which];
+    const int64_t x = ((int64_t)blockIdx.x - (which ? a.of[which - 1].blocks : 0)) * 256 + threadIdx.x;
+    if (x >= g.quads) return;
+    if (g.cu && !a.zero_rest) {
         int64_t s;
         int len;
-        seq_range(a.cuk, a.N, a.N, a.Tk, s, len);
-        if (x * 4 / a.Dr >= s) return;
+        seq_range(g.cu, a.N, a.N, g.T, s, len);
+        if (x / g.row_quads >= s) return;
     }
     f32x4 sum = {0.f, 0.f, 0.f, 0.f};
-    const float* p = a.dkr_part + 4 * x;
+    const float* p = g.in + 4 * x;
 #pragma unroll 8
-    for (int h = 0; h < a.H; ++h) {
-        const f32x4 v = *reinterpret_cast<const f32x4*>(p + h * per);
+    for (int i = 0; i < g.n; ++i) {
+        const f32x4 v = *reinterpret_cast<const f32x4*>(p + 4 * i * g.quads);
 #pragma unroll
         for (int j = 0; j < 4; ++j) sum[j] += v[j];
     }
-    T* o = static_cast<T*>(a.dkr) + 4 * x;
+    T* o = static_cast<T*>(g.out) + 4 * x;
 #pragma unroll
     for (int j = 0; j < 4; ++j) o[j] = (T)sum[j];
 }
@@ -212,7 +233,7 @@ template <class T, int DN, int DR> hipError_t launch_dq(const MlaArgs& a, hipStr
     int64_t slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 128);
     if (slots * a.H < kSmallLaunch<T>) {
         slots = tile_slots(a.cuq, a.B, a.N, a.Tq, 32);
-        mla_dq_kernel<T, DN, DR, true><<<dim3((unsigned)(slots * a.H)), 256, 0, s>>>(a, slots);
+        mla_dq_kernel<T, DN, DR, true><<<dim3((unsigned)(slots * a.H * a.q_parts)), 256, 0, s>>>(a, slots);
     } else {
         mla_dq_kernel<T, DN, DR, false><<<dim3((unsigned)(slots * a.H)), 256, 0, s>>>(a, slots);
     }
@@ -222,19 +243,61 @@ template <class T> hipError_t launch_dq_dims(const MlaArgs& a, hipStream_t s) {
     if (a.Dn == 128) return a.Dr ? launch_dq<T, 128, 64>(a, s) : launch_dq<T, 128, 0>(a, s);
     return a.Dr ? launch_dq<T, 64, 64>(a, s) : launch_dq<T, 64, 0>(a, s);
 }
-template <class T> hipError_t launch_dkr(const MlaArgs& a, hipStream_t s) {
-    const int64_t quads = (int64_t)a.B * a.Tk * a.Dr / 4;
-    if (quads == 0) return hipSuccess;
-    mla_dkr_kernel<T><<<dim3((unsigned)((quads + 255) / 256)), 256, 0, s>>>(a, quads);
+template <class T> hipError_t launch_sums(const MlaArgs& a, hipStream_t s) {
+    SharesArgs x{};
+    x.N = a.N;
+    x.zero_rest = a.zero_rest;
+    int64_t blocks = 0;
+    const auto add = [&](Shares& g, const float* in, void* out, int n, int row, int T_, const int32_t* cu) {
+        g.in = in; g.out = out; g.n = n; g.row_quads = row; g.T = T_; g.cu = cu;
+        g.quads = in ? (int64_t)a.B * T_ * row : 0;
+        g.blocks = blocks += (g.quads + 255) / 256;
+    };
+    add(x.of[0], a.dkr ? a.dkr_part : nullptr, a.dkr, a.k_parts * a.H, a.Dr / 4, a.Tk, a.cuk);
+    add(x.of[1], a.k_parts > 1 ? a.dkv_part : nullptr, a.dkv, a.k_parts, a.H * a.Dn / 2, a.Tk, a.cuk);
+    add(x.of[2], a.q_parts > 1 ? a.dq_part : nullptr, a.dq, a.q_parts, a.H * (a.Dn + a.Dr) / 4, a.Tq, a.cuq);
+    if (blocks == 0) return hipSuccess;
+    mla_sum_kernel<T><<<dim3((unsigned)blocks), 256, 0, s>>>(x);
     return hipGetLastError();
 }
 
 }  // namespace
 
+// Workgroups that share a block of queries (keys), each with every so many
+// groups of four tiles of the other side: as many as find a compute unit, if the
+// walk is long enough to be worth a sum of their shares. Measured, 128 + 64
+// channels, causal, the backward with and without: float32 500 tokens, 8 heads
+// 71 : 107 us, 1000 tokens, 1 head 70 : 186, 200 tokens 47 : 63. bf16 1000
+// tokens, 1 head 35 : 50, 4000 tokens 98 : 154, but 500 tokens, 8 heads 39 : 35.
+static int walk_parts(bool bf16, int64_t workgroups, int T) {
+    const int tiles = (T + 31) / 32, least = bf16 ? 16 : 4;
+    int p = 1;
+    while (p < 4 && workgroups > 0 && workgroups * p * 2 <= 256 && tiles > least * p) p *= 2;
+    return p;
+}
+size_t mla_bwd_plan(MlaArgs& a) {
+    a.q_parts = walk_parts(a.bf16, tile_slots(a.cuq, a.B, a.N, a.Tq, 32) * a.H, a.Tk);
+    a.k_parts = walk_parts(a.bf16, tile_slots(a.cuk, a.B, a.N, a.Tk, 32) * a.H, a.Tq);
+    const int64_t nq = (int64_t)a.B * a.H * a.Tq, nk = (int64_t)a.B * a.H * a.Tk;
+    float* p = a.delta;
+    const auto take = [&](int64_t n) {
+        float* x = p;
+        if (p) p += n;
+        return x;
+    };
+    const int64_t sizes[] = {(nq + 3) / 4 * 4, a.k_parts * nk * a.Dr, a.q_parts > 1 ? a.q_parts * nq * (a.Dn + a.Dr) : 0,
+                             a.k_parts > 1 ? a.k_parts * nk * 2 * a.Dn : 0};
+    a.delta = take(sizes[0]);
+    a.dkr_part = take(sizes[1]);
+    a.dq_part = take(sizes[2]);
+    a.dkv_part = take(sizes[3]);
+    return (size_t)(sizes[0] + sizes[1] + sizes[2] + sizes[3]) * sizeof(float);
+}
+
 hipError_t launch_mla_bwd(const MlaArgs& a, hipStream_t s) {
     hipError_t e = a.bf16 ? launch_dq_dims<__bf16>(a, s) : launch_dq_dims<float>(a, s);
     if (e == hipSuccess) e = a.bf16 ? launch_mla_dkv_bf16(a, s) : launch_dkv_dims<float>(a, s);
-    if (e == hipSuccess) e = a.bf16 ? launch_dkr<__bf16>(a, s) : launch_dkr<float>(a, s);
+    if (e == hipSuccess) e = a.bf16 ? launch_sums<__bf16>(a, s) : launch_sums<float>(a, s);
     return e;
 }
 

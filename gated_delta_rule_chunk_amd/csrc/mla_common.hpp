@@ -353,7 +353,7 @@ __device__ __forceinline__ f32x16 sum_blocks(const char* regions, int stride, in
     return s;
 }
 
-// Which head and which slot of the tile list a workgroup takes. Workgroups are
+// Which head and which slot of the tile list workgroup `item` takes. Workgroups are
 // dealt round-robin over the 8 XCDs, each with an L2 of its own, and start in
 // the order of their index. Heads go fastest, so that with a multiple of 8 of
 // them every head stays on one XCD, where its tiles share the L2; slots go by
@@ -361,8 +361,7 @@ __device__ __forceinline__ f32x16 sum_blocks(const char* regions, int stride, in
 // each from its longest tile, left a fifth of the wave slots empty at 4096
 // tokens); and 32 heads go at a time, 4 on an XCD, so that enough of a head's
 // tiles walk through the same keys together.
-__device__ __forceinline__ void head_and_slot(int64_t slots, int H, int& h, int64_t& slot) {
-    const int64_t item = blockIdx.x;
+__device__ __forceinline__ void head_and_slot(int64_t item, int64_t slots, int H, int& h, int64_t& slot) {
     const int g = (int)(item / (32 * slots)) * 32, n = H - g < 32 ? H - g : 32;
     const int64_t r = item - g * slots;
     h = g + (int)(r % n);

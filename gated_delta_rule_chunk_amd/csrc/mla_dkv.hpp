@@ -30,7 +30,8 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
     const int n32 = lane & 31, hf = lane >> 5, lw = SPLIT ? 0 : w;
     int h;
     int64_t slot;
-    head_and_slot(slots, a.H, h, slot);
+    const int part = SPLIT ? (int)(blockIdx.x / (slots * a.H)) : 0;
+    head_and_slot(blockIdx.x - part * slots * a.H, slots, a.H, h, slot);
     int n, k0, Lq, Lk;
     int64_t qs, ks;
     if (!tile_of(a.cuk, a.N, a.Tk, BK, slot, lane, n, ks, Lk, k0)) return;
@@ -145,15 +146,20 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
     const bool live = j < Lk;
     T* p = static_cast<T*>(a.dkv) + kvrow * 2 * DN;
     float* r = nullptr;
-    if constexpr (DR > 0) r = a.dkr_part + (((int64_t)h * a.B + (a.cuk ? 0 : n)) * a.Tk + (a.cuk ? ks + jc : jc)) * DR;
+    if constexpr (DR > 0) r = a.dkr_part + ((((int64_t)part * a.H + h) * a.B + (a.cuk ? 0 : n)) * a.Tk + (a.cuk ? ks + jc : jc)) * DR;
     // block d of the results: dk, then dv
+    float* f = SPLIT && a.k_parts > 1 ? a.dkv_part + ((int64_t)part * a.B * a.Tk * a.H + kvrow) * 2 * DN : nullptr;
     auto store = [&](int d, const f32x16& x) {
+        if (SPLIT && f && (d < NV || d >= NK)) {
+            store_tile<float>(f + (d < NV ? 32 * d : DN + 32 * (d - NK)), x, d < NV ? a.scale : 1.f, hf, live);
+            return;
+        }
         if (d < NV) store_tile<T>(p + 32 * d, x, a.scale, hf, live);
         else if (d < NK) store_tile<float>(r + 32 * (d - NV), x, a.scale, hf, live);
         else store_tile<T>(p + DN + 32 * (d - NK), x, 1.f, hf, live);
     };
     if constexpr (SPLIT) {
-        for (int t = w; t < tiles; t += 4) {
+        for (int t = w + 4 * part; t < tiles; t += 4 * a.k_parts) {
             load(t, smem[w]);
             const int row = first + t * BQ + n32;
             const float ls = row_lse(row), dl = row_delta(row);
@@ -214,7 +220,7 @@ template <class T, int DN, int DR> hipError_t launch_dkv(const MlaArgs& a, hipSt
     int64_t slots = tile_slots(a.cuk, a.B, a.N, a.Tk, 128);
     if (slots * a.H < kSmallLaunch<T>) {
         slots = tile_slots(a.cuk, a.B, a.N, a.Tk, 32);
-        mla_dkv_kernel<T, DN, DR, true><<<dim3((unsigned)(slots * a.H)), 256, 0, s>>>(a, slots);
+        mla_dkv_kernel<T, DN, DR, true><<<dim3((unsigned)(slots * a.H * a.k_parts)), 256, 0, s>>>(a, slots);
     } else {
         mla_dkv_kernel<T, DN, DR, false><<<dim3((unsigned)(slots * a.H)), 256, 0, s>>>(a, slots);
     }

@@ -35,7 +35,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_fwd_kernel(Ml
     const int n32 = lane & 31, hf = lane >> 5, lw = SPLIT ? 0 : w;
     int h;
     int64_t slot;
-    head_and_slot(slots, a.H, h, slot);
+    head_and_slot(blockIdx.x, slots, a.H, h, slot);
     slot = slots - 1 - slot;                            // a sequence's longest rows of keys first
     int n, q0, Lq, Lk;
     int64_t qs, ks;

@@ -128,6 +128,29 @@ def test_rows_behind_the_last_sequence():
         assert torch.equal(x[:, :n], y[:, :n]) and bool((x[:, n:] == 7).all())
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("Dn,Dr", DIMS)
+def test_backward_in_parts(dtype, Dn, Dr):
+    """Few workgroups and long walks: several workgroups share a block, and their results are summed."""
+    lens = [(1100, 1100), (0, 0), (40, 650), (33, 20)]
+    q, kv, kr, d_o, cuq, cuk = _make(lens, 1, Dn, Dr, dtype, 19, tail=70, grad=True)
+    nq, nk = 1173, 1770
+    for t, n in ((q, nq), (d_o, nq), (kv, nk)) + (((kr, nk),) if Dr else ()):
+        t[:, n:] = float("nan")
+    got = _both(q, kv, kr, d_o, cuq, cuk, lens, True)
+    names = ["dq", "dkv"] + (["dk_rope"] if Dr else [])
+    o, lse = kda.mla_fwd(q, kv, kr, cuq, cuk)
+    grads = {x: torch.full_like(got[x], 7.0) for x in names}
+    kda.mla_bwd(q, kv, kr, o, lse, d_o, cuq, cuk, **grads)
+    for x in names:
+        n = nq if x == "dq" else nk
+        assert int(got[x][:, n:].count_nonzero()) == 0
+        assert torch.equal(grads[x][:, :n], got[x][:, :n]) and bool((grads[x][:, n:] == 7).all())
+    lens = [(1100, 1100)]
+    _both(q[:, :1100].clone(), kv[:, :1100].clone(), None if kr is None else kr[:, :1100], d_o[:, :1100].clone(), None,
+          None, lens, False)
+
+
 def test_nan_in_a_hidden_key_stays_hidden():
     lens = [(100, 100)]
     q, kv, kr, d_o, cuq, cuk = _make(lens, 2, 128, 64, BF16, 10, grad=True)

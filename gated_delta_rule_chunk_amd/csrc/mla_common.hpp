@@ -72,22 +72,24 @@ template <int RC> __device__ __forceinline__ int swizzle(int r) {
 // Written as an instruction so that the compiler, which cannot tell the two
 // buffers apart, does not wait for the next tile before it reads this one;
 // wait_loads_and_lds() and the barrier order them. It has no register output.
-// The compiler inserts no wait states here either, so the asm brings them.
+// The compiler inserts no wait states here either, so the asm brings them: one
+// between the write of m0, the place in LDS, and the load. Nothing else in these
+// kernels uses m0 (the compiler takes no reserved register as a clobber).
 __device__ __forceinline__ void load_lds16(const char* g, char* lds) {
     const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(KDA_LDS char*)lds);
-    asm volatile("s_mov_b32 m0, %0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(base), "v"(g) : "memory");
+    asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off" ::"s"(base), "v"(g) : "memory");
 }
 // the same from g (uniform) + off bytes. A load needs five wait states after a
 // vector instruction has written its scalar address (readfirstlane does), but
 // none after a scalar one, whose own read of it the hardware orders: the
-// address is copied.
+// address is copied, which is m0's wait state too.
 __device__ __forceinline__ void load_lds16s(const char* g, int off, char* lds) {
     const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(KDA_LDS char*)lds);
     const uint64_t u = reinterpret_cast<uint64_t>(g);
     const uint64_t from = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32 |
                           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u);
     uint64_t t;
-    asm volatile("s_mov_b64 %0, %3\n\ts_mov_b32 m0, %1\n\tglobal_load_lds_dwordx4 %2, %0"
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dwordx4 %2, %0"
                  : "=&s"(t)
                  : "s"(base), "v"(off), "s"(from)
                  : "memory");
@@ -101,7 +103,7 @@ __device__ __forceinline__ void load_lds16s_if(bool on, const char* g, int off, 
                           (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u);
     const uint32_t lanes = __builtin_amdgcn_readfirstlane(on ? 0xffffffffu : 0u);
     uint64_t t;
-    asm volatile("s_mov_b64 %0, %3\n\ts_mov_b32 m0, %1\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\t"
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\ts_mov_b32 exec_lo, %4\n\ts_mov_b32 exec_hi, %4\n\t"
                  "global_load_lds_dwordx4 %2, %0\n\ts_mov_b64 exec, -1"
                  : "=&s"(t)
                  : "s"(base), "v"(off), "s"(from), "s"(lanes)

@@ -118,6 +118,25 @@ def test_scalar_base_written_by_a_vector_instruction(kernels):
     assert not bad, bad
 
 
+def test_m0_written_before_the_load(kernels):
+    """One wait state between a write of m0 and a load into LDS, which takes its place there from m0."""
+    bad = {}
+    for fn, code, i, _ in _loads(kernels):
+        states, name, o = next(_back(code, i))
+        if o and o[0] == "m0":
+            bad[fn] = bad.get(fn, 0) + 1
+    assert not bad, bad
+
+
+def test_m0_has_no_other_use(kernels):
+    """The loads of the latent-attention kernels change m0, which the compiler does not know."""
+    for fn in {fn for fn, *_ in _loads(kernels) if "mla" in fn}:
+        for i, (name, ops) in enumerate(kernels[fn]):
+            if "m0" in ops:
+                assert (name, ops[0]) == ("s_mov_b32", "m0"), (fn, name, ops)
+                assert any("_load_lds_" in x for x, _ in kernels[fn][i + 2:i + 5]), fn
+
+
 def test_no_lane_is_left_out(kernels):
     """A load issued under a changed exec mask is followed by its restoration, which nothing comes between."""
     for fn, code, i, _ in _loads(kernels):

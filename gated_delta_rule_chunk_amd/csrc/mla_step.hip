@@ -123,20 +123,19 @@ __device__ __forceinline__ void store4(float* p, const f32x4& x, float mul) {
     *reinterpret_cast<f32x4*>(p) = f32x4{x[0] * mul, x[1] * mul, x[2] * mul, x[3] * mul};
 }
 
-// The list of tiles, 64 sequences at a time, one per lane: rows of
-// the cache (cut to what the page table holds), tiles, and tiles up to and with
-// the sequence's.
+// The list of tiles, 64 sequences at a time, one per lane: the length, by which
+// tokens see, rows of the cache (the length cut to what the page table holds),
+// tiles, and tiles up to and with the sequence's.
 struct Scan {
-    int len, cnt, sum;
-    bool over;                  // the length says more than the table holds
+    int len, rows, cnt, sum;
     __device__ __forceinline__ int all() const { return __builtin_amdgcn_readlane(sum, 63); }
 };
 __device__ __forceinline__ Scan scan_tiles(const MlaStepArgs& a, int b0, int lane) {
     Scan x;
     const int cap = a.max_pages << a.page_shift, n = b0 + lane < a.Nb ? a.lens[b0 + lane] : 0;
-    x.over = n > cap;
-    x.len = n < 0 ? 0 : x.over ? cap : n;
-    x.cnt = (x.len + kTile - 1) / kTile;
+    x.len = n < 0 ? 0 : n;
+    x.rows = x.len < cap ? x.len : cap;
+    x.cnt = (x.rows + kTile - 1) / kTile;
     x.sum = x.cnt;
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) {
@@ -252,10 +251,11 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
         const int l = __ffsll((unsigned long long)__ballot(before + sq.sum > at)) - 1;
         const int b = b0 + l;
         const int tiles = __builtin_amdgcn_readlane(sq.cnt, l), len = __builtin_amdgcn_readlane(sq.len, l);
+        const int rows = __builtin_amdgcn_readlane(sq.rows, l);
         const int first = before + __builtin_amdgcn_readlane(sq.sum, l) - tiles;    // the sequence's place in the list
         const int t0 = at - first, t1 = end - first < tiles ? end - first : tiles;
         at = first + t1;
-        if (t0 == 0 && group == 0 && w == 0 && lane == l && sq.over) atomicAdd(a.status, 1u);
+        if (t0 == 0 && group == 0 && w == 0 && lane == 0 && len > rows) atomicAdd(a.status, 1u);
 
         // queries: row 16 WAVES group + 16 w + n of the (token, head) pairs
         const int row = (group * WAVES + w) * 16 + (lane & 15), mrow = row < M ? row : M - 1;
@@ -275,13 +275,13 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
             const char *lo, *hi;
         };
         // Page table entries of 64 pages, one per lane; -1 for no such page or one
-        // past the length. A tile's halves lie in one page or, where pages have
+        // past the rows. A tile's halves lie in one page or, where pages have
         // 16 rows, in an even one and the next: of the same 64.
         const int32_t* table = a.table + (int64_t)b * a.max_pages;
         int pbase = -64, pages = 0;
         auto entry = [&](int p) {
             const int i = p + lane;
-            return i < a.max_pages && (int64_t)i << ps < len ? table[i] : 0;
+            return i < a.max_pages && (int64_t)i << ps < rows ? table[i] : 0;
         };
         auto keep = [&](int p, int e) {
             pbase = p;
@@ -290,7 +290,7 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
             // counted once: where the page's first row is this part's
             const uint64_t bad = __ballot(e < 0 && r >= t0 * kTile && r < (int64_t)t1 * kTile);
             if (bad && group == 0 && w == 0 && lane == 0) atomicAdd(a.status, (unsigned)__popcll(bad));
-            pages = r < len ? e : -1;
+            pages = r < rows ? e : -1;
         };
         // the first entries and the queries are under way together
         const int p0 = t0 * kTile >> ps, e = entry(p0);
@@ -308,14 +308,14 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
             const int mask = (1 << ps) - 1;
             Tile x;
             x.have = (e0 >= 0 ? 1 : 0) | (e1 >= 0 ? 2 : 0);
-            x.whole = x.have == 3 && k0 + kTile <= len;
+            x.whole = x.have == 3 && k0 + kTile <= rows;
             // (a missing page's address is not used)
             x.lo = static_cast<const char*>(a.cache) + (((int64_t)e0 << ps) + (k0 & mask)) * (RC * 16);
             x.hi = static_cast<const char*>(a.cache) + (((int64_t)e1 << ps) + ((k0 + 16) & mask)) * (RC * 16);
             return x;
         };
         auto load_edge = [&](const Tile& x, int t, char* to) {
-            const int rmax = len - 1 - t * kTile;
+            const int rmax = rows - 1 - t * kTile;
             load_edge_tile<T, RC, WAVES>(to, x.lo, x.hi, rmax < kTile - 1 ? rmax : kTile - 1, x.have, w, lane);
         };
         constexpr int kLoads = tile_loads<T, RC, WAVES>();
@@ -389,8 +389,8 @@ __global__ __launch_bounds__(64 * WAVES, WAVES > 4 ? 2 : 1) void mla_step_kernel
                 for (int r = 0; r < 4; ++r) sc[q][r] += odd[q][r];
             // keys that this lane's token sees in the tile: the first lim + 1
             const int k0 = t * kTile;
-            if (k0 + kTile > len - a.Tq + 1 || have != 3) {
-                const int lim = len - a.Tq + tok - k0 - 4 * g;
+            if (k0 + kTile > len - a.Tq + 1 || k0 + kTile > rows || have != 3) {
+                const int last = len - a.Tq + tok < rows - 1 ? len - a.Tq + tok : rows - 1, lim = last - k0 - 4 * g;
 #pragma unroll
                 for (int q = 0; q < 2; ++q)
 #pragma unroll

@@ -383,6 +383,26 @@ def test_missing_pages_are_reported(page):
 
 
 @pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("T,page", [(4, 16), (3, 32), (5, 64)])
+def test_length_past_the_page_table_hides_its_rows_only(dtype, T, page):
+    """Each token sees what it sees by the length given, of the rows that the table holds."""
+    cap, H = 3 * page, 7
+    lens = [cap, cap + 1, cap + T - 1, cap + 50, 10 ** 9, cap - 1]
+    cache, table, rows = _cache([cap] * len(lens), page, 256, 64, dtype, 22)
+    ql, qr = _queries(len(lens), T, H, 256, 64, dtype, 23)
+    o, lse = kda.mla_step(ql, qr, cache, table, torch.tensor(lens, dtype=torch.int32, device="cuda"), scale=0.07)
+    with pytest.raises(kda.KDAError, match="4 counted"):
+        kda.device_check()
+    t = torch.arange(T, device="cuda").repeat_interleave(H)
+    for b, n in enumerate(lens):
+        k = rows[b][None]
+        r = mla_ref.attend(torch.cat((ql[b], qr[b]), -1).reshape(1, T * H, -1), k, k[..., :256], 0.07,
+                           (n - T + t + 1).clamp(0, cap), dtype=dtype)
+        mla_ref.check(f"o[{b}]", o[b].reshape(1, T * H, 256), r["o"])
+        mla_ref.check(f"lse[{b}]", lse[b].reshape(1, T * H), r["lse"])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
 @pytest.mark.parametrize("Dc,Dr,page", [(512, 64, 16), (256, 0, 64)])
 @pytest.mark.parametrize("packed", [False, True])
 def test_append(dtype, Dc, Dr, page, packed):

@@ -4,6 +4,7 @@
 
 #include "../../include/kda_mla.h"
 #include "launchers.hpp"
+#include "mla_common.hpp"
 
 namespace {
 
@@ -39,6 +40,18 @@ kda_status check_scale(const char* fn, float scale) {
 // possible, only of what the kernels' 16-byte accesses need.
 bool stride_ok(int64_t s, kda_dtype dtype) { return s >= 0 && s * (dtype == KDA_BF16 ? 2 : 4) % 16 == 0; }
 
+// A launch counts its threads in 32 bits: so many workgroups of 256.
+constexpr int64_t kMaxGrid = 0xffffffffll / 256;
+
+// The expanded kernels take a workgroup per head and tile of 128 rows (small
+// launches of 32 rows: far from the limit) of a side's queries or keys.
+kda_status check_tiles(const char* fn, const int32_t* cu, int32_t B, int32_t N, int32_t T, int32_t H) {
+    if (kda::mla::tile_slots(cu, B, N, T, 128) > kMaxGrid / H)
+        return fail(KDA_ERR_UNSUPPORTED, "%s: problem too large: over %lld tiles of 128 rows, heads counted", fn,
+                    (long long)kMaxGrid);
+    return KDA_OK;
+}
+
 // Checks shared by the forward and the backward; fills a on success.
 kda_status check_expanded(const char* fn, const void* q, const void* kv, const void* k_rope, int64_t kr_row,
                           int64_t kr_batch, const int32_t* cuq, const int32_t* cuk, int32_t B, int32_t Tq, int32_t Tk,
@@ -66,11 +79,8 @@ kda_status check_expanded(const char* fn, const void* q, const void* kv, const v
                     (long long)kr_row, (long long)kr_batch);
     if (!aligned(q) || !aligned(kv) || !aligned(k_rope))
         return fail(KDA_ERR_INVALID_ARG, "%s: q, kv and k_rope must be 16-byte aligned", fn);
-    // the kernels count workgroups in 31 bits
-    const int64_t rows = (Tq > Tk ? Tq : Tk) / 128 + 1;
-    if (((int64_t)(cuq ? 1 : B) * rows + N) * H > ((int64_t)1 << 30))
-        return fail(KDA_ERR_UNSUPPORTED, "%s: problem too large", fn);
-    // and the bytes of a tile's 64 rows in 31
+    if (kda_status st = check_tiles(fn, cuq, B, N, Tq, H)) return st;
+    // the kernels hold the bytes of a tile's 64 rows in 31 bits
     if (H > 4096 || (Dr && kr_row > (1 << 22)))
         return fail(KDA_ERR_UNSUPPORTED, "%s: H=%d, k_rope row stride %lld; at most 4096 and 2^22 elements", fn, H,
                     (long long)kr_row);
@@ -154,6 +164,9 @@ kda_status kda_mla_bwd(const void* q, const void* kv, const void* k_rope, int64_
     if (kda_status st = check_expanded(fn, q, kv, k_rope, k_rope_row, k_rope_batch, cu_seqlens_q, cu_seqlens_k, B, Tq,
                                        Tk, H, Dn, Dr, N, causal, scale, dtype, zero_rest, a))
         return st;
+    if (kda_status st = check_tiles(fn, cu_seqlens_k, B, N, Tk, H)) return st;
+    if (Dr && (int64_t)B * Tk > kMaxGrid * 256 / 16)      // the sum of dk_rope: a thread for each 4 of its columns
+        return fail(KDA_ERR_UNSUPPORTED, "%s: problem too large: B * Tk = %lld", fn, (long long)B * Tk);
     if (Tq == 0 && Tk == 0) return KDA_OK;
     if (Tq > 0 && (!o || !lse || !d_o || !dq))
         return fail(KDA_ERR_INVALID_ARG, "%s: o, lse, d_o and dq must be non-NULL when Tq > 0", fn);
@@ -204,6 +217,9 @@ kda_status kda_mla_cache_append(const void* latent, int64_t latent_row, int64_t 
     if (kda_status st = check_cache(fn, cache, page_table, cache_lens, n_pages, page_size, max_pages, Dc, Dr, dtype,
                                     a.page_shift))
         return st;
+    // a thread for each 16 bytes of a token
+    if ((int64_t)B * T > kMaxGrid * 256 / ((Dc + Dr) * (dtype == KDA_BF16 ? 2 : 4) / 16))
+        return fail(KDA_ERR_UNSUPPORTED, "%s: problem too large: B * T = %lld", fn, (long long)B * T);
     if (!latent || (Dr == 0) != (k_rope == nullptr))
         return fail(KDA_ERR_INVALID_ARG, "%s: latent must be non-NULL, k_rope NULL if and only if Dr = 0", fn);
     if (!stride_ok(latent_row, dtype) || !stride_ok(latent_batch, dtype) ||
@@ -211,7 +227,6 @@ kda_status kda_mla_cache_append(const void* latent, int64_t latent_row, int64_t 
         !aligned(k_rope))
         return fail(KDA_ERR_INVALID_ARG, "%s: latent and k_rope must be 16-byte aligned, strides included", fn);
     if (latent == cache || k_rope == cache) return fail(KDA_ERR_INVALID_ARG, "%s: cache must not alias an input", fn);
-    if ((int64_t)B * T > ((int64_t)1 << 30)) return fail(KDA_ERR_UNSUPPORTED, "%s: problem too large", fn);
     a.latent = latent; a.lat_row = latent_row; a.lat_batch = latent_batch;
     a.kr = k_rope; a.kr_row = k_rope_row; a.kr_batch = k_rope_batch;
     a.cache = cache; a.table = page_table; a.lens = cache_lens; a.cu = cu_seqlens;
@@ -277,6 +292,8 @@ kda_status kda_mla_step(const void* q_latent, int64_t q_latent_n, int64_t q_late
     a.n_pages = n_pages; a.max_pages = max_pages; a.Nb = Nb; a.Tq = Tq; a.H = H; a.Dc = Dc; a.Dr = Dr;
     a.scale = scale; a.bf16 = dtype == KDA_BF16;
     const size_t need = kda::mla_step_plan(a);
+    const int64_t joins = (int64_t)Nb * ((Tq * H + a.join_rows - 1) / a.join_rows);     // workgroups of the second kernel
+    if (joins > kMaxGrid) return fail(KDA_ERR_UNSUPPORTED, "%s: problem too large: Nb = %d", fn, Nb);
     if (!workspace || workspace_bytes < need || !aligned(workspace))
         return fail(KDA_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed, 16-byte aligned", fn,
                     workspace ? workspace_bytes : 0, need);

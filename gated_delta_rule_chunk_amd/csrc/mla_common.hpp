@@ -448,7 +448,7 @@ __device__ __forceinline__ bool tile_of(const int32_t* cu, int N, int T, int til
 }
 // length of that list, at most
 inline int64_t tile_slots(const int32_t* cu, int B, int N, int T, int tile) {
-    return cu ? (int64_t)T / tile + N + 1 : (int64_t)B * ((T + tile - 1) / tile);
+    return cu ? (int64_t)T / tile + N + 1 : B * (((int64_t)T + tile - 1) / tile);
 }
 
 }  // namespace mla

@@ -65,7 +65,9 @@ extern "C" {
  *   o       [B,Tq,H,Dn] dtype;  lse [B,H,Tq] float32, or NULL
  * Neither may alias an input. Every tensor pointer is 16-byte aligned.
  * Supported: Dn in {64, 128}, Dr in {0, 64}, KDA_BF16 and KDA_F32, H <= 4096,
- * k_rope_row <= 2^22; sizes past what the offsets hold are refused.
+ * k_rope_row <= 2^22. A launch holds 2^24 - 1 workgroups: more tiles of 128
+ * query rows of a sequence times H are refused (packed: Tq / 128 + N + 1 tiles);
+ * in the backward, of key rows too, and, with Dr > 0, B * Tk past 2^28 - 16.
  * Tq = 0 is a no-op; with Tk = 0, kv and k_rope may be NULL.
  */
 kda_status kda_mla_fwd(const void* q, const void* kv, const void* k_rope, int64_t k_rope_row, int64_t k_rope_batch,
@@ -117,7 +119,8 @@ kda_status kda_mla_bwd(const void* q, const void* kv, const void* k_rope, int64_
  *          sequence are not written; or NULL: N = B, T new tokens each
  * Two tokens of one call must not land in the same cache row (sequences that
  * share the page they grow into): which one stays is then not defined.
- * B * T = 0 is a no-op. Dc in {256, 512}, Dr in {0, 64}.
+ * B * T = 0 is a no-op. Dc in {256, 512}, Dr in {0, 64}. B * T tokens of over
+ * 2^32 - 256 16-byte chunks together are refused.
  */
 kda_status kda_mla_cache_append(const void* latent, int64_t latent_row, int64_t latent_batch, const void* k_rope,
                                 int64_t k_rope_row, int64_t k_rope_batch, void* cache, const int32_t* page_table,
@@ -138,7 +141,8 @@ kda_status kda_mla_cache_append(const void* latent, int64_t latent_row, int64_t 
  *            aligned; calls that may run at the same time need their own
  *   o        [Nb,Tq,H,Dc] dtype, in latent space;  lse [Nb,Tq,H] float32 or NULL
  * scale finite and > 0 (the expanded head's, 1 / sqrt(Dn + Dr), not Dc's).
- * Nb * Tq = 0 is a no-op. Dc in {256, 512}, Dr in {0, 64}.
+ * Nb * Tq = 0 is a no-op. Dc in {256, 512}, Dr in {0, 64}. At most: Tq * H
+ * 2^20, Nb * Tq * H 2^30, Nb 2^24 - 1.
  */
 size_t kda_mla_step_workspace_bytes(int32_t Nb, int32_t Tq, int32_t H, int32_t Dc, int32_t page_size,
                                     int32_t max_pages, kda_dtype dtype);

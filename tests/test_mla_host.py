@@ -95,6 +95,34 @@ def test_bwd_refuses(lib, kw, status, needle):
     assert needle in lib.kda_last_error_message().decode()
 
 
+# A launch holds at most (2^32 - 1) / 256 workgroups of 256 threads. Each pair: refused, and one step below,
+# which passes the check of the sizes and is refused for a missing pointer.
+MOST = (2 ** 32 - 1) // 256
+PACKED = dict(B=1, cuq=P[10], cuk=P[11])
+
+
+@pytest.mark.parametrize("kw,less", [
+    (dict(H=128, N=MOST // 128, **PACKED), dict(N=MOST // 128 - 1)),                    # (100 / 128 + N + 1) * H
+    (dict(H=96, Tq=128 * 1000, N=MOST // 96 - 1000, **PACKED), dict(N=MOST // 96 - 1001)),
+    (dict(H=16, B=MOST // 32 + 1, N=MOST // 32 + 1, Tq=129), dict(Tq=128)),             # B * ceil(Tq / 128) * H
+    (dict(H=1, B=2 ** 31 - 1, N=2 ** 31 - 1, Tq=128 * MOST), dict(B=1, N=1)),
+])
+def test_fwd_refuses_more_workgroups_than_a_launch_holds(lib, kw, less):
+    assert _fwd(lib, **kw) == UNSUP and "too large" in lib.kda_last_error_message().decode()
+    assert _fwd(lib, o=None, **{**kw, **less}) == BAD and "o must" in lib.kda_last_error_message().decode()
+
+
+@pytest.mark.parametrize("kw,less", [
+    (dict(H=128, N=MOST // 128, **PACKED), dict(N=MOST // 128 - 1)),
+    (dict(H=16, B=MOST // 32 + 1, N=MOST // 32 + 1, Tq=129), dict(Tq=128)),
+    (dict(H=16, B=MOST // 32 + 1, N=MOST // 32 + 1, Tk=129), dict(Tk=128)),             # the keys' side alone
+    (dict(H=1, B=1, N=1, Tk=MOST * 16 + 1), dict(Tk=MOST * 16)),                        # the sum of the shared key part
+])
+def test_bwd_refuses_more_workgroups_than_a_launch_holds(lib, kw, less):
+    assert _bwd(lib, **kw) == UNSUP and "too large" in lib.kda_last_error_message().decode()
+    assert _bwd(lib, dq=None, **{**kw, **less}) == BAD and "non-NULL" in lib.kda_last_error_message().decode()
+
+
 def test_bwd_workspace_bytes(lib):
     w = kda.mla_bwd_workspace_bytes
     assert w(2, 100, 50, 4, 64) == 2 * 4 * 100 * 4 + 4 * 2 * 50 * 64 * 4
@@ -130,6 +158,13 @@ def test_append_refuses(lib, kw, status, needle):
     assert needle in lib.kda_last_error_message().decode()
 
 
+def test_append_refuses_more_workgroups_than_a_launch_holds(lib):
+    """A thread a chunk of 16 bytes, 72 of them a token."""
+    t = MOST * 256 // 72
+    assert _append(lib, B=1, N=1, T=t + 1) == UNSUP and "too large" in lib.kda_last_error_message().decode()
+    assert _append(lib, B=1, N=1, T=t, lat=None) == BAD and "latent" in lib.kda_last_error_message().decode()
+
+
 def _step(lib, **kw):
     a = dict(ql=P[0], ln=2048, lt=2048, lh=512, qr=P[1], rn=256, rt=256, rh=64, cache=P[2], table=P[3], lens=P[4],
              n_pages=9, page=16, max_pages=3, B=4, T=1, H=4, Dc=512, Dr=64, scale=0.1, dtype=kda.KDA_BF16, ws=P[5],
@@ -150,6 +185,12 @@ def _step(lib, **kw):
 def test_step_refuses(lib, kw, status, needle):
     assert _step(lib, **kw) == status
     assert needle in lib.kda_last_error_message().decode()
+
+
+def test_step_refuses_more_workgroups_than_a_launch_holds(lib):
+    """The join takes a workgroup a sequence at least."""
+    assert _step(lib, B=MOST + 1, H=1) == UNSUP and "too large" in lib.kda_last_error_message().decode()
+    assert _step(lib, B=MOST, H=1, ws=None) == BAD and "workspace" in lib.kda_last_error_message().decode()
 
 
 def test_step_workspace_bytes(lib):

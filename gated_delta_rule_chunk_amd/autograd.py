@@ -11,8 +11,10 @@ same function, so its gradient is the same backward call's. ``mla`` pairs the
 expanded latent attention's calls (kda_mla_fwd / kda_mla_bwd). Every step runs in
 the library's kernels: this module saves the inputs, routes the incoming
 gradients to the backward call and casts the float32 gradients to each input's
-dtype.
+dtype. Gradients of gradients are refused (RuntimeError).
 """
+import functools
+
 import torch
 
 from . import (chunk_bwd, chunk_bwd_conv, chunk_bwd_prologue, chunk_fwd, chunk_fwd_conv, chunk_fwd_prologue,
@@ -25,6 +27,37 @@ def _contig(t):
 
 def _cast(grad, like):
     return None if grad is None or like is None else grad.to(like.dtype)
+
+
+class _FirstOrder(torch.autograd.Function):
+    """Passes n gradients on as functions of the tensors behind them, with no
+    gradient of their own."""
+
+    @staticmethod
+    def forward(ctx, n, *tensors):
+        return tuple(t.detach() for t in tensors[:n])
+
+    @staticmethod
+    def backward(ctx, *grads):
+        raise RuntimeError("the backward calls of this library have no second-order gradient")
+
+
+def _first_order(backward):
+    """For a ``backward`` that runs in the library's kernels, which autograd does
+    not see into: where it keeps a graph of the gradients (create_graph), a
+    gradient of them raises, instead of passing for zero."""
+
+    @functools.wraps(backward)
+    def wrapped(ctx, *d):
+        with torch.no_grad():
+            grads = backward(ctx, *d)
+        if not torch.is_grad_enabled():
+            return grads
+        have = [g for g in grads if g is not None]
+        have = iter(_FirstOrder.apply(len(have), *have, *d, *ctx.saved_tensors))
+        return tuple(None if g is None else next(have) for g in grads)
+
+    return wrapped
 
 
 class _Chunk(torch.autograd.Function):
@@ -41,6 +74,7 @@ class _Chunk(torch.autograd.Function):
         return o, fin
 
     @staticmethod
+    @_first_order
     def backward(ctx, d_o, d_fin):
         q, k, v, g, beta, s0, cu = ctx.saved_tensors
         dq, dk, dv, dg, db, d0 = chunk_bwd(q, k, v, g, beta, _contig(d_o), initial_state=s0,
@@ -66,6 +100,7 @@ class _ChunkPrologue(torch.autograd.Function):
         return o, fin
 
     @staticmethod
+    @_first_order
     def backward(ctx, d_o, d_fin):
         q, k, v, gl, bl, A_log, dt_bias, s0, cu = ctx.saved_tensors
         scale, lb, eps = ctx.args
@@ -90,6 +125,7 @@ class _ChunkConv(torch.autograd.Function):
         return (o, fin) + tuple(conv_fin)
 
     @staticmethod
+    @_first_order
     def backward(ctx, d_o, d_fin, d_cq, d_ck, d_cv):
         xq, xk, xv, wq, wk, wv, gl, bl, A_log, dt_bias, s0, cs_q, cs_k, cs_v, cu = ctx.saved_tensors
         scale, lb, eps, act = ctx.args
@@ -141,6 +177,7 @@ class _Mla(torch.autograd.Function):
         return o
 
     @staticmethod
+    @_first_order
     def backward(ctx, d_o):
         q, kv, k_rope, cu_q, cu_k, o, lse = ctx.saved_tensors
         causal, scale = ctx.args

@@ -49,10 +49,10 @@ def _first_order(backward):
 
     @functools.wraps(backward)
     def wrapped(ctx, *d):
+        if not torch.is_grad_enabled():
+            return backward(ctx, *d)
         with torch.no_grad():
             grads = backward(ctx, *d)
-        if not torch.is_grad_enabled():
-            return grads
         have = [g for g in grads if g is not None]
         have = iter(_FirstOrder.apply(len(have), *have, *d, *ctx.saved_tensors))
         return tuple(None if g is None else next(have) for g in grads)

@@ -25,6 +25,12 @@ def _contig(t):
     return None if t is None else t.contiguous()
 
 
+def _aligned(t):
+    """Contiguous and 16-byte aligned, a copy where t is not (autograd hands on slices of other gradients)."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _cast(grad, like):
     return None if grad is None or like is None else grad.to(like.dtype)
 
@@ -181,7 +187,7 @@ class _Mla(torch.autograd.Function):
     def backward(ctx, d_o):
         q, kv, k_rope, cu_q, cu_k, o, lse = ctx.saved_tensors
         causal, scale = ctx.args
-        dq, dkv, dkr = mla_bwd(q, kv, k_rope, o, lse, _contig(d_o), cu_seqlens_q=cu_q, cu_seqlens_k=cu_k,
+        dq, dkv, dkr = mla_bwd(q, kv, k_rope, o, lse, _aligned(d_o), cu_seqlens_q=cu_q, cu_seqlens_k=cu_k,
                                causal=causal, scale=scale)
         return dq, dkv, dkr, None, None, None, None
 

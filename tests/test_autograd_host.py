@@ -65,3 +65,17 @@ def test_a_graph_of_first_gradients_alone_is_no_error(entry, monkeypatch):
     frozen = [t.detach() for t in x[1:]]
     g, = torch.autograd.grad(f(leaves[0], *frozen).sum(), leaves[:1])
     assert torch.equal(g, torch.ones_like(g))
+
+
+def test_an_incoming_gradient_off_its_alignment_is_copied(monkeypatch):
+    """kda_mla_bwd takes 16-byte aligned rows; a slice that autograd hands on (here of a concatenation's
+    gradient) need not be."""
+    seen = []
+    f, x = _mla(monkeypatch)
+    monkeypatch.setattr(autograd, "mla_bwd", lambda q, kv, r, o, lse, d_o, **_: seen.append(d_o) or _like(q, kv, r))
+    leaves = [t.requires_grad_() for t in x]
+    o = f(*leaves)
+    w = torch.arange(3.0 + o.numel())
+    (torch.cat((torch.ones(3), o.flatten())) * w).sum().backward()
+    assert seen[0].is_contiguous() and seen[0].data_ptr() % 16 == 0
+    assert torch.equal(seen[0].flatten(), w[3:])

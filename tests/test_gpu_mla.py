@@ -220,6 +220,35 @@ def test_gradient_against_differences():
         assert abs(have - quot[0]) <= slack + (ref[name][1] * d.abs()).sum().item(), name
 
 
+@pytest.mark.parametrize("dtype", [BF16, F32])
+def test_offsets_past_31_bits_and_largest_strides(dtype):
+    """q, kv and their gradients of over 2^31 elements, with the most heads and the widest rows of k_rope that
+    are supported. The first and the last head against 64 bits; the incoming gradient of the others is zero, so
+    that the sum over the heads is these two's."""
+    H, Tq, Tk, row = 4096, 2800, 2200, 1 << 22
+    g = torch.Generator(device="cuda").manual_seed(24)
+
+    def rand(*shape):
+        return torch.randn(shape, generator=g, device="cuda", dtype=dtype)
+
+    q, kv = rand(1, Tq, H, 192), rand(1, Tk, H, 256)
+    assert q.numel() > 1 << 31 and kv.numel() > 1 << 31
+    kr = torch.empty((Tk - 1) * row + 64, dtype=dtype, device="cuda").as_strided((1, Tk, 64), (row * Tk, row, 1))
+    kr.copy_(rand(1, Tk, 64))
+    ends = [0, H - 1]
+    d_o = torch.zeros(1, Tq, H, 128, dtype=dtype, device="cuda")
+    d_o[:, :, ends] = rand(1, Tq, 2, 128)
+    o, lse = kda.mla_fwd(q, kv, kr)
+    dq, dkv, dkr = kda.mla_bwd(q, kv, kr, o, lse, d_o)
+    ref = mla_ref.expanded(q[:, :, ends], kv[:, :, ends], kr, [(Tq, Tk)], True, 192 ** -0.5, d_o[:, :, ends])
+    for name, x in (("o", o[:, :, ends]), ("lse", lse[:, ends]), ("dq", dq[:, :, ends]), ("dkv", dkv[:, :, ends]),
+                    ("dk_rope", dkr)):
+        mla_ref.check(name, x, ref[name])
+    assert int(dq[:, :, 1:-1].count_nonzero()) == 0 and int(dkv[:, :, 1:-1].count_nonzero()) == 0
+    del q, kv, kr, d_o, o, lse, dq, dkv, dkr, ref
+    torch.cuda.empty_cache()
+
+
 # ---- cache ------------------------------------------------------------------------------------------------------
 
 

@@ -252,11 +252,11 @@ struct MlaArgs {
     void* dq;
     void* dkv;
     void* dkr;                  // [B,Tk,Dr] contiguous, nullptr when Dr = 0
-    float* delta;               // workspace [B,H,Tq]: sum of d_o * o over a row
+    float* delta;               // workspace [delta_parts,B,H,Tq]: sum of d_o * o over a row, in parts to be added
     float* dkr_part;            // workspace [k_parts,H,B,Tk,Dr]: per-head gradients of the shared key part
     // split kernels: workgroups that share a block of queries (keys), each with
     // a float32 result of its own: workspace [q_parts,B,Tq,H,Dn+Dr], [k_parts,B,Tk,H,2*Dn]
-    int32_t q_parts, k_parts;
+    int32_t q_parts, k_parts, delta_parts;
     float* dq_part;
     float* dkv_part;
 };

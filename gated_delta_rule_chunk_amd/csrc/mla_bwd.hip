@@ -17,10 +17,19 @@
 // causal, 4096 tokens, 96 heads of 128 + 64 channels: 745-790 us for dq (512
 // products a score and head: 1050-1110 TFLOP/s), 1170-1330 us for dk and dv (640:
 // 780-880 TFLOP/s), 18 us for the sum over the heads (100 MB read, 5.6 TB/s).
-// Rounding: bf16 operands are rounded once, p and ds among them; D comes from
-// o as the forward returned it. An independent error of up to 2^-9 of each ds
-// leaves dq with about the error that its own rounding has (0.0017 of its
-// norm), 0.0025 together.
+// Rounding: bf16 operands are rounded once, p and ds among them. An independent
+// error of up to 2^-8 of each ds (0.0017 in the mean square) leaves dq with about
+// the error that its own rounding has, 0.0024 of its norm together.
+// D from o as the forward rounded it to bf16 would be off by up to 2^-8 of the
+// magnitudes in it, for all keys of a row alike: 0.003 of the norm of dq and dk
+// in sequences of 2 to 8 tokens, 0.006 in long ones whose weights are nearly all
+// on one key. As sum_j p_ij = 1, the sum of a row's ds says what D is off by, so
+// the first kernel hands D + sum_j ds_ij to the second one, and walks tiles of
+// up to 128 keys, where most of the gradient's norm is, twice, the first time for
+// D alone. What is left is dq of rows of more keys with such weights: taking it
+// out would take the walk's products again (a second walk for all: 0.6 ms of
+// 2.5) or sum_j p_ij k_j beside dq, whose registers are full. The same time as
+// without, within 1% (a step of 4096 tokens, 96 heads 2480-2525 us, packed 327).
 #include "launchers.hpp"
 #include "mla_common.hpp"
 #include "mla_dkv.hpp"
@@ -37,7 +46,9 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_
     constexpr int kK = BN * CK * 16, kR = BN * CR * 16, kTileBytes = 2 * kK + kR;
     constexpr int kBuf = SPLIT ? larger(kTileBytes, DQ * 128) : kTileBytes;    // split: also the exchange
     constexpr int kLoaders = SPLIT ? 1 : 4;
+    constexpr bool kRounded = sizeof(T) == 2;                                  // o has lost what D needs
     __shared__ __attribute__((aligned(1024))) char smem[SPLIT ? 4 : 2][kBuf];
+    __shared__ float dsum[2][SPLIT ? 4 : 1][32];                               // split: the waves' sums for D
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int n32 = lane & 31, hf = lane >> 5, lw = SPLIT ? 0 : w;
     int h;
@@ -68,7 +79,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_
     const int i = wq0 + n32, ic = i < Lq ? i : Lq - 1;
     const bool live = i < Lq;
     const int64_t qrow = (qs + ic) * a.H + h;
-    const int64_t srow = ((a.cuq ? 0 : (int64_t)n * a.H) + h) * a.Tq + (a.cuq ? qs + ic : ic);
+    const int64_t srow0 = ((a.cuq ? 0 : (int64_t)n * a.H) + h) * a.Tq + (a.cuq ? qs : 0), srow = srow0 + ic;
     Frag<T> qf[DQ / 16], df[DN / 16];
     float delta = 0.f;
     {
@@ -85,11 +96,22 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_
             for (int j = 0; j < 8; ++j) delta += (float)df[s][j] * (float)of[j];
         }
         delta = half_sum(delta);
-        if (live && hf == 0 && !rest && part == 0 && w == (SPLIT ? 0 : w)) a.delta[srow] = delta;
     }
+    // this lane's row, for addresses that are formed after the loop and not kept over it
+    auto row_again = [&] {
+        int r = ic;
+        if constexpr (kRounded) asm volatile("" : "+v"(r));
+        return r;
+    };
+    auto put_delta = [&](float x) {
+        if (live && hf == 0 && !rest && part < a.delta_parts && w == (SPLIT ? 0 : w))
+            a.delta[(int64_t)part * a.B * a.H * a.Tq + srow0 + row_again()] = x;
+    };
+    if constexpr (!kRounded) put_delta(delta);
     f32x16 acc[DQ / 32];
 #pragma unroll
     for (int d = 0; d < DQ / 32; ++d) acc[d] = zero16();
+    float more = 0.f;                                   // sum of this lane's ds: what D is off by
     const float c = a.scale * kLog2e;
     // a row without a visible key has lse -inf; all its terms are hidden below
     const float lse = rest ? 0.f : a.lse[srow], l2 = lse == -INFINITY ? 0.f : lse * kLog2e;
@@ -147,6 +169,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_
             for (int r = 0; r < 16; ++r) {
                 const float p = __builtin_amdgcn_exp2f(__builtin_fmaf(sc[r], c, -l2));
                 sc[r] = p * (dp[r] - delta);
+                if constexpr (kRounded) more += sc[r];
             }
             const Frag<T> f[2] = {to_frag<T>(sc, 0), to_frag<T>(sc, 1)};
             ahead.run(read, [&](int i, const Frag<T>& x) {
@@ -154,35 +177,75 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_
             });
         }
     };
-    T* p = static_cast<T*>(a.dq) + qrow * DQ;
+    // Tiles of up to 128 keys are walked twice, the first time for D.
+    int pass = tiles <= 128 / BN ? 0 : 1;
+    auto again = [&](float x) {                         // D's correction, from all of a row's products
+        if (pass == 0) {
+            delta += x;
+            more = 0.f;
+#pragma unroll
+            for (int d = 0; d < DQ / 32; ++d) acc[d] = zero16();
+        }
+        return pass++ == 0;
+    };
     if constexpr (SPLIT) {
-        for (int t = w + 4 * part; t < tiles; t += 4 * a.q_parts) {
-            load(t, smem[w]);
-            wait_loads_and_lds();
-            compute(t, smem[w]);
-            wait_loads_and_lds();
+        auto walk = [&](int t0, int step) {
+            for (int t = t0; t < tiles; t += step) {
+                load(t, smem[w]);
+                wait_loads_and_lds();
+                compute(t, smem[w]);
+                wait_loads_and_lds();
+            }
+        };
+        float x;
+        if constexpr (kRounded) {
+            do {                                        // (a first walk is a whole one, parts or not)
+                walk(w + (pass ? 4 * part : 0), pass ? 4 * a.q_parts : 4);
+                more = half_sum(more);
+                if (hf == 0) dsum[pass][w][n32] = more;
+                wait_loads_and_lds();
+                wg_barrier();
+                x = ((dsum[pass][0][n32] + dsum[pass][1][n32]) + dsum[pass][2][n32]) + dsum[pass][3][n32];
+            } while (again(x));
+            put_delta((part == 0 ? delta : 0.f) + x);
+        } else {
+            walk(w + 4 * part, 4 * a.q_parts);
         }
 #pragma unroll
         for (int d = 0; d < DQ / 32; ++d) put_block(smem[w], d, acc[d], lane);
         wait_loads_and_lds();
         wg_barrier();
         const float one[4] = {1.f, 1.f, 1.f, 1.f};
-        float* f = a.q_parts > 1 ? a.dq_part + (((int64_t)part * a.B * a.Tq * a.H) + qrow) * DQ : nullptr;
+        const int64_t out = (qs + row_again()) * a.H + h;
+        T* p = static_cast<T*>(a.dq) + out * DQ;
+        float* f = a.q_parts > 1 ? a.dq_part + (((int64_t)part * a.B * a.Tq * a.H) + out) * DQ : nullptr;
         for (int d = w; d < DQ / 32; d += 4) {
             const f32x16 x = sum_blocks(smem[0], kBuf, d, one, lane);
             if (f) store_tile<float>(f + 32 * d, x, a.scale, hf, live);
             else store_tile<T>(p + 32 * d, x, a.scale, hf, live);
         }
     } else {
-        if (tiles > 0) load(0, smem[0]);
-        wait_loads_and_lds();
-        wg_barrier();
-        for (int t = 0; t < tiles; ++t) {
-            if (t + 1 < tiles) load(t + 1, smem[(t + 1) & 1]);
-            compute(t, smem[t & 1]);
+        auto walk = [&] {
+            if (tiles > 0) load(0, smem[0]);
             wait_loads_and_lds();
             wg_barrier();
+            for (int t = 0; t < tiles; ++t) {
+                if (t + 1 < tiles) load(t + 1, smem[(t + 1) & 1]);
+                compute(t, smem[t & 1]);
+                wait_loads_and_lds();
+                wg_barrier();
+            }
+        };
+        if constexpr (kRounded) {
+            do {
+                walk();
+                more = half_sum(more);
+            } while (again(more));
+            put_delta(delta + more);
+        } else {
+            walk();
         }
+        T* p = static_cast<T*>(a.dq) + ((qs + row_again()) * a.H + h) * DQ;
 #pragma unroll
         for (int d = 0; d < DQ / 32; ++d) store_tile<T>(p + 32 * d, acc[d], a.scale, hf, live);
     }
@@ -285,7 +348,9 @@ size_t mla_bwd_plan(MlaArgs& a) {
         if (p) p += n;
         return x;
     };
-    const int64_t sizes[] = {(nq + 3) / 4 * 4, a.k_parts * nk * a.Dr, a.q_parts > 1 ? a.q_parts * nq * (a.Dn + a.Dr) : 0,
+    a.delta_parts = a.bf16 ? a.q_parts : 1;
+    const int64_t sizes[] = {(a.q_parts * nq + 3) / 4 * 4, a.k_parts * nk * a.Dr,
+                             a.q_parts > 1 ? a.q_parts * nq * (a.Dn + a.Dr) : 0,
                              a.k_parts > 1 ? a.k_parts * nk * 2 * a.Dn : 0};
     a.delta = take(sizes[0]);
     a.dkr_part = take(sizes[1]);

@@ -90,7 +90,14 @@ __global__ __launch_bounds__(256, 1) void mla_dkv_kernel(MlaArgs a, int64_t slot
         const float x = r < Lq ? a.lse[srow + r] * kLog2e : INFINITY;
         return x == -INFINITY ? INFINITY : x;
     };
-    auto row_delta = [&](int r) { return r < Lq ? a.delta[srow + r] : 0.f; };
+    auto row_delta = [&](int r) {
+        if (r >= Lq) return 0.f;
+        const float* d = a.delta + srow + r;
+        float x = *d;
+        if constexpr (sizeof(T) == 2)
+            for (int p = 1; p < a.delta_parts; ++p) x += *(d += (int64_t)a.B * a.H * a.Tq);
+        return x;
+    };
     // stats(qb, g, l2, de): lse and D of rows 8 g + 4 hf .. + 3 of query block qb
     auto compute = [&](int t, const char* buf, auto stats) {
 #pragma unroll

@@ -151,6 +151,57 @@ def test_backward_in_parts(dtype, Dn, Dr):
           None, lens, False)
 
 
+def _gradients_with_exact_d(q, k, v, d_o, scale, limit):
+    """dq, dk of one head in 64 bits, and how far they may be off where D_i = sum_j p_ij dp_ij carries no rounding
+    to bf16: mla_ref.attend's bounds without the term of the rounded o, and with the float32 roundings of D's
+    own terms and sum instead."""
+    f, h, u = torch.float64, mla_ref.H32, mla_ref.half_step(BF16)
+    q, k, v, d = q.to(f), k.to(f), v.to(f), d_o.to(f)
+    E, n = v.shape[-1], (q.shape[0] + k.shape[0] + 8) * h
+    seen = torch.arange(k.shape[0], device=q.device)[None] < limit[:, None]
+    s = (q @ k.t() * scale).masked_fill(~seen, -math.inf)
+    lse = torch.logsumexp(s, -1, keepdim=True)
+    p = torch.exp(s - lse)
+    mag = (q.abs() @ k.abs().t()) * scale
+    err = torch.where(seen, (q.shape[-1] + 4) * h * mag + 4 * h * s.abs(), 0.0)
+    rel = err.amax(-1, keepdim=True) + 4 * h * lse.abs() + 8 * h
+    dp, dpm = d @ v.t(), d.abs() @ v.abs().t()
+    delta = (p * dp).sum(-1, keepdim=True)
+    size = dp.abs() + 2 * delta.abs()
+    term = (4 * rel + 4 * h) * size + (E + 4) * h * dpm
+    be = (p * (term + n * size)).sum(-1, keepdim=True) * 2
+    ds = p * (dp - delta)
+    bds = (p * (term + be) * (1 + 4 * rel) + u * ds.abs()) * (1 + u)
+    dq, dk, dsa = scale * (ds @ k), scale * (ds.t() @ q), ds.abs() + bds
+    return {"dq": (dq, scale * (bds @ k.abs() + n * (dsa @ k.abs())) + u * dq.abs()),
+            "dk": (dk, scale * (bds.t() @ q.abs() + n * (dsa.t() @ q.abs())) + u * dk.abs())}
+
+
+@pytest.mark.parametrize("Dn,Dr", DIMS)
+@pytest.mark.parametrize("H,lens,scale", [(3, [(2, 2), (33, 33), (128, 128), (60, 128), (7, 3), (100, 120)], 0.5),
+                                          (61, [(2, 2), (65, 65), (128, 128), (130, 130), (1, 90)], 0.5),
+                                          (3, [(300, 300), (129, 400)], 0.7), (61, [(300, 300), (129, 400)], 0.7)])
+def test_backward_forms_d_itself(Dn, Dr, H, lens, scale):
+    """Where one key has nearly all of a row's weight, the row's gradient is small beside its D, and D from o as
+    it was rounded to bf16 would be off by as much as the gradient. dk (and dk_rope with one head) never goes by
+    it, dq does not in tiles of up to 128 keys."""
+    q, kv, kr, d_o, cuq, cuk = _make(lens, H, Dn, Dr, BF16, 30, grad=True)
+    o, lse = kda.mla_fwd(q, kv, kr, cuq, cuk, scale=scale)
+    dq, dkv, _ = kda.mla_bwd(q, kv, kr, o, lse, d_o, cuq, cuk, scale=scale)
+    a = b = 0
+    for Lq, Lk in lens:
+        rq, rk = slice(a, a + Lq), slice(b, b + Lk)
+        i = torch.arange(max(0, Lq - Lk), Lq, device="cuda")          # rows before see nothing
+        for h in (0, H - 1):
+            k = kv[0, rk, h, :Dn] if kr is None else torch.cat((kv[0, rk, h, :Dn], kr[0, rk]), -1)
+            ref = _gradients_with_exact_d(q[0, rq, h][i], k, kv[0, rk, h, Dn:], d_o[0, rq, h][i], scale,
+                                          i + Lk - Lq + 1)
+            if Lk <= 128:
+                mla_ref.check(f"dq {Lq} {Lk} {h}", dq[0, rq, h][i], ref["dq"])
+            mla_ref.check(f"dk {Lq} {Lk} {h}", dkv[0, rk, h, :Dn], tuple(x[:, :Dn] for x in ref["dk"]))
+        a, b = a + Lq, b + Lk
+
+
 def test_nan_in_a_hidden_key_stays_hidden():
     lens = [(100, 100)]
     q, kv, kr, d_o, cuq, cuk = _make(lens, 2, 128, 64, BF16, 10, grad=True)

@@ -226,10 +226,15 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 && !SPLIT ? 2 : 1) void mla_dq_
         }
     } else {
         auto walk = [&] {
-            if (tiles > 0) load(0, smem[0]);
+            // the compiler does not know where a walk begins: what it would form
+            // in front of both walks and keep pushes operands out of the registers
+            // (a quarter of the kernel's time with one workgroup a compute unit)
+            int t0 = 0;
+            if constexpr (kRounded) asm volatile("" : "+s"(t0));
+            if (tiles > 0) load(t0, smem[t0]);
             wait_loads_and_lds();
             wg_barrier();
-            for (int t = 0; t < tiles; ++t) {
+            for (int t = t0; t < tiles; ++t) {
                 if (t + 1 < tiles) load(t + 1, smem[(t + 1) & 1]);
                 compute(t, smem[t & 1]);
                 wait_loads_and_lds();

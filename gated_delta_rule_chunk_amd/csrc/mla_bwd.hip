@@ -15,8 +15,8 @@
 // order, from float32 shares; in launches of few workgroups several of them
 // share a block, and it sums their results too. Bound by the matrix cores; measured, bf16,
 // causal, 4096 tokens, 96 heads of 128 + 64 channels: 745-790 us for dq (512
-// products a score and head: 1050-1110 TFLOP/s), 1170-1330 us for dk and dv (640:
-// 780-880 TFLOP/s), 18 us for the sum over the heads (100 MB read, 5.6 TB/s).
+// products a score and head: 1050-1110 TFLOP/s), 1140-1330 us for dk and dv (640:
+// 780-910 TFLOP/s), 18 us for the sum over the heads (100 MB read, 5.6 TB/s).
 // Rounding: bf16 operands are rounded once, p and ds among them. An independent
 // error of up to 2^-8 of each ds (0.0017 in the mean square) leaves dq with about
 // the error that its own rounding has, 0.0024 of its norm together.
@@ -27,9 +27,11 @@
 // the first kernel hands D + sum_j ds_ij to the second one, and walks tiles of
 // up to 128 keys, where most of the gradient's norm is, twice, the first time for
 // D alone. What is left is dq of rows of more keys with such weights: taking it
-// out would take the walk's products again (a second walk for all: 0.6 ms of
-// 2.5) or sum_j p_ij k_j beside dq, whose registers are full. The same time as
-// without, within 1% (a step of 4096 tokens, 96 heads 2480-2525 us, packed 327).
+// out would take the walk's products again (a second walk for all: 0.7 ms of
+// 2.5) or sum_j p_ij k_j beside dq, whose registers are full. The backward takes
+// as long as without, within 1%, at 4096 tokens and 96 heads (1960-1995 us), 512
+// tokens and 16 heads times 8 (102), and packed ragged batches; 64 sequences of
+// 100 tokens, 16 heads, all walked twice, 127 against 115 us.
 #include "launchers.hpp"
 #include "mla_common.hpp"
 #include "mla_dkv.hpp"
@@ -337,6 +339,10 @@ template <class T> hipError_t launch_sums(const MlaArgs& a, hipStream_t s) {
 // channels, causal, the backward with and without: float32 500 tokens, 8 heads
 // 71 : 107 us, 1000 tokens, 1 head 70 : 186, 200 tokens 47 : 63. bf16 1000
 // tokens, 1 head 35 : 50, 4000 tokens 98 : 154, but 500 tokens, 8 heads 39 : 35.
+// T is the rows of all packed sequences: the host does not know their lengths,
+// and their mean misjudges a long one among short ones. Total against mean, 1
+// head: float32 1000 tokens and 15 times 8 70 : 188, 16 of 64 48 : 44, 4 of 256
+// 49 : 46; bf16 2000 and 20 times 50 59 : 86, 32 of 64 26 : 21, 2 of 2000 63 : 62.
 static int walk_parts(bool bf16, int64_t workgroups, int T) {
     const int tiles = (T + 31) / 32, least = bf16 ? 16 : 4;
     int p = 1;

@@ -336,13 +336,23 @@ __device__ __forceinline__ void wait_loads_and_lds() {
 // Split kernels: where a launch would leave compute units idle, the four waves
 // of a workgroup take the same 32 rows and every fourth tile of the other side
 // each, with a tile buffer of their own, and their sums meet in LDS at the end.
-// A launch counts as small below one workgroup per compute unit; in float32,
-// whose products hide the loads that are not overlapped here, below 1.75.
-// Measured, 8 heads of 128 + 64 channels, causal, split against whole in us,
-// forward and backward: bf16 2048 tokens (128 workgroups) 30 : 46, 110 : 158;
-// 192 workgroups 44 : 65, 214 : 221; 256 71 : 87, 334 : 296; 376 141 : 135,
-// 678 : 447. float32 128 workgroups 123 : 332, 408 : 1255; 256 440 : 657, 1488 :
-// 2500; 376 921 : 960, 3116 : 3691; 512 1683 : 1393, 5687 : 5374.
+// A launch counts as small below one workgroup of 128 rows per compute unit; in
+// float32, whose products hide the loads that are not overlapped here, below 1.75.
+// Measured, causal, split against whole in us, forward, backward:
+//   workgroups          128               256               384               512
+//   2048 tokens, 128 + 64 channels
+//     bf16      32 : 48, 120 : 158   43 : 48, 212 : 159   62 : 52, 318 : 169   81 : 56, 420 : 193
+//     float32 121 : 332, 405 : 1258 242 : 334, 803 : 1275 365 : 336, 1215 : 1289 482 : 365, 1599 : 1399
+//   2048 tokens, 64 channels
+//     bf16      17 : 30, 53 : 102    20 : 32, 86 : 103    29 : 33, 127 : 109   34 : 33, 167 : 111
+//     float32   54 : 146, 186 : 497  82 : 146, 279 : 498 117 : 182, 407 : 555 152 : 193, 525 : 603
+//   8 sequences of 512, 128 + 64 channels
+//     bf16      16 : 17, 69 : 56     26 : 18, 113 : 60    36 : 24, 166 : 92    42 : 26, 201 : 100
+//     float32   65 : 89, 214 : 342   99 : 93, 328 : 349  140 : 159, 471 : 602 171 : 180, 581 : 686
+// The two sides cross at other numbers for each direction, width and length; one
+// per type serves them all, and leaves up to a third to some near it: bf16
+// backwards of 512 tokens are faster whole at 128, bf16 forwards of 2048 split
+// at 256, float32 ones of 64 channels split at 512.
 template <class T> constexpr int64_t kSmallLaunch = sizeof(T) == 4 ? 448 : 256;
 
 // A wave's accumulator block d to and from its exchange region
@@ -369,11 +379,14 @@ __device__ __forceinline__ f32x16 sum_blocks(const char* regions, int stride, in
 // Which head and which slot of the tile list workgroup `item` takes. Workgroups are
 // dealt round-robin over the 8 XCDs, each with an L2 of its own, and start in
 // the order of their index. Heads go fastest, so that with a multiple of 8 of
-// them every head stays on one XCD, where its tiles share the L2; slots go by
-// falling work, so that no long tile starts last (heads one after the other,
+// them every head stays on one XCD, where its tiles share the L2; a sequence's slots
+// go by falling work, so that no long tile starts last (heads one after the other,
 // each from its longest tile, left a fifth of the wave slots empty at 4096
 // tokens); and 32 heads go at a time, 4 on an XCD, so that enough of a head's
-// tiles walk through the same keys together.
+// tiles walk through the same keys together. Sequences follow one another as the
+// caller packed them (the dq kernel and the forward take the last one first), so
+// a long one may still start last: the tiles of twelve ragged sequences of up to
+// 1100 tokens, 24 heads, would end about a fifth sooner in falling order.
 __device__ __forceinline__ void head_and_slot(int64_t item, int64_t slots, int H, int& h, int64_t& slot) {
     const int g = (int)(item / (32 * slots)) * 32, n = H - g < 32 ? H - g : 32;
     const int64_t r = item - g * slots;

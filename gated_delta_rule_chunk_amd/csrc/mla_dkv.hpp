@@ -4,7 +4,8 @@
 // their accumulators: mla_dkv_bf16.hip and mla_bwd.hip.
 // One wave per SIMD: keys, values and the two accumulators of 32 keys take 240
 // of its registers, so its matrix and vector instructions do not overlap and the
-// matrix cores are busy 37% of the time. Two things that shorten other loops
+// matrix cores are busy 37-39% of the time. The split kernels of 128 + 64 channels
+// spill, float32's 4 registers, bf16's 1. Two things that shorten other loops
 // here lengthen this one (bf16, 4096 tokens, 96 heads): the next tile's loads
 // issued among the products 1517 against 1303 us, the scores' operands read a
 // fixed six ahead 1400.

@@ -8,11 +8,14 @@
 // keys in tiles of BN. The key and value tiles go straight from
 // global memory to LDS, two buffers, the next tile in flight while one is
 // computed; queries, scores, probabilities and outputs stay in registers (the
-// scores are formed transposed: mla_common.hpp). Bound by the matrix cores and
+// scores are formed transposed: mla_common.hpp). In bf16 the probabilities are
+// rounded once, as operands, their sum is not: the matrix cores take bf16, and
+// the result is off by 0.0020-0.0023 of its norm where its own rounding alone
+// leaves 0.0017. Bound by the matrix cores and
 // the exponentials, 2 (2 Dn + Dr) products per score: a wave's own matrix and
 // vector instructions hardly overlap, those of the two waves on a SIMD do.
-// Measured, bf16, causal, 4096 tokens, 96 heads of 128 + 64 channels: 505-565
-// us, 910-1020 TFLOP/s over the visible pairs (a plain 8192^3 product of the
+// Measured, bf16, causal, 4096 tokens, 96 heads of 128 + 64 channels: 484-565
+// us, 910-1060 TFLOP/s over the visible pairs (a plain 8192^3 product of the
 // library: 1131), matrix cores busy 55% of the time, no bank conflicts.
 #include "launchers.hpp"
 #include "mla_common.hpp"
@@ -120,7 +123,8 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_fwd_kernel(Ml
         mx = half_max(mx);
         // The running maximum moves only when some row's grows by more than
         // 2^8 (from -inf at first): until then its terms reach at most 2^8,
-        // exact enough in float32, and the output needs no rescaling.
+        // exact enough in float32, and the output needs no rescaling (the
+        // published conditional rescaling of the online softmax).
         if (__any((mx - m) * c > 8.f)) {
             const float mn = fmaxf(m, mx), ms = mn == -INFINITY ? 0.f : mn;   // nothing seen yet: all terms are 0
             const float al = __builtin_amdgcn_exp2f((m - ms) * c);

@@ -27,8 +27,9 @@
  * and sums in float32, probabilities and score gradients rounded to bf16 once
  * as operands of the second product (relative to the norm of the result, an
  * error of about 0.0017 each, next to the 0.0017 of the result's own rounding).
- * The rounding of o stays out of the backward, but for dq of rows that see over
- * 128 keys and have nearly all their weight on one (up to 0.006 of the norm).
+ * The rounding of o stays out of the backward, but for dq of rows (in blocks of
+ * 128 of which one sees over 128 keys) with nearly all their weight on one key:
+ * up to 0.006 of the norm.
  * KDA_F32 runs on the float32 matrix cores.
  *
  * Preconditions that are not checked: finite inputs; cu_seqlens starting at 0
@@ -83,7 +84,10 @@ kda_status kda_mla_fwd(const void* q, const void* kv, const void* k_rope, int64_
  *   q, kv, k_rope, cu_seqlens, sizes, causal, scale, dtype  as in the forward
  *   o, lse     what the forward returned;  d_o [B,Tq,H,Dn] dtype
  *   workspace  at least kda_mla_bwd_workspace_bytes(...) bytes of device
- *              memory, 16-byte aligned; contents on entry do not matter
+ *              memory, 16-byte aligned; contents on entry do not matter. Mostly
+ *              the heads' shares of dk_rope, 4 * B * H * Tk * Dr bytes (96 heads:
+ *              24 KB a key); small calls up to four times that and as many
+ *              float32 gradients, for any dtype
  *   dq [B,Tq,H,Dn+Dr], dkv [B,Tk,H,2*Dn], dk_rope [B,Tk,Dr] (contiguous; NULL
  *              if and only if Dr = 0) dtype. Sums are float32, rounded to
  *              dtype at the end; the sum of dk_rope over the heads is float32
@@ -140,7 +144,10 @@ kda_status kda_mla_cache_append(const void* latent, int64_t latent_row, int64_t 
  *            and heads (_h) in elements, multiples of 16 bytes, channels
  *            contiguous (a head-major product's output, or a slice)
  *   workspace  at least kda_mla_step_workspace_bytes(...) bytes, 16-byte
- *            aligned; calls that may run at the same time need their own
+ *            aligned; calls that may run at the same time need their own. It
+ *            grows with Tq * H past 1024 rows (64 float32 results a row: 13 GB at
+ *            1024 tokens of 96 heads, Dc = 512): this call is for few new tokens,
+ *            the expanded form for many
  *   o        [Nb,Tq,H,Dc] dtype, in latent space;  lse [Nb,Tq,H] float32 or NULL
  * scale finite and > 0 (the expanded head's, 1 / sqrt(Dn + Dr), not Dc's).
  * Nb * Tq = 0 is a no-op. Dc in {256, 512}, Dr in {0, 64}. At most: Tq * H

@@ -25,8 +25,8 @@
 // in sequences of 2 to 8 tokens, 0.006 in long ones whose weights are nearly all
 // on one key. As sum_j p_ij = 1, the sum of a row's ds says what D is off by, so
 // the first kernel hands D + sum_j ds_ij to the second one, and walks tiles of
-// up to 128 keys, where most of the gradient's norm is, twice, the first time for
-// D alone. What is left is dq of rows of more keys with such weights: taking it
+// up to 128 keys, where that error weighs most, twice, the first time for D
+// alone. What is left is dq of rows of more keys with such weights: taking it
 // out would take the walk's products again (a second walk for all: 0.7 ms of
 // 2.5) or sum_j p_ij k_j beside dq, whose registers are full. The backward takes
 // as long as without, within 1%, at 4096 tokens and 96 heads (1960-1995 us), 512

@@ -3,9 +3,9 @@ beside its plain form.
 
 A cache row is a token's latent c and, in rotary models, a key part r that the
 heads share. Five operators: the write of new rows into a cache that holds the
-latents in 4 bits (``mla_cache_append_q4``) and the read of rows back from it
-(``mla_cache_read_q4``), measured together; the absorbed attention of new tokens
-over that cache (``mla_step_q4``); the accumulated attention weight of cached
+latents in 4 bits (``mla_cache_append_mx``) and the read of rows back from it
+(``mla_cache_read_mx``), measured together; the absorbed attention of new tokens
+over that cache (``mla_step_mx``); the accumulated attention weight of cached
 rows (``mla_weigh``); and the eviction of the rows of least weight
 (``mla_evict``).
 
@@ -358,12 +358,12 @@ def run(s):
             _plain_weigh(s) if kind == "weigh" else _plain_evict(s)
     import gated_delta_rule_chunk_amd as kda
     if kind == "store":
-        kda.mla_cache_append_q4(s["latent"], s["k_rope"], s["cache"], s["table"], s["lens"], cu_seqlens=s["cu"])
-        x, r = kda.mla_cache_read_q4(s["cache"], s["table"], s["cu_back"], s["rows_back"], case["latent"],
+        kda.mla_cache_append_mx(s["latent"], s["k_rope"], s["cache"], s["table"], s["lens"], cu_seqlens=s["cu"])
+        x, r = kda.mla_cache_read_mx(s["cache"], s["table"], s["cu_back"], s["rows_back"], case["latent"],
                                      _TYPES[case["dtype"]], starts=s["from"])
         return (x,) if r is None else (x, r)
     if kind == "step":
-        return kda.mla_step_q4(s["q_latent"], s["q_rope"], s["cache"], s["table"], s["lens"], scale=_scale(case))
+        return kda.mla_step_mx(s["q_latent"], s["q_rope"], s["cache"], s["table"], s["lens"], scale=_scale(case))
     if kind == "weigh":
         return kda.mla_weigh(s["q_latent"], s["q_rope"], s["cache"], s["table"], s["lens"], s["lse"], _scale(case),
                              s["weights"], out=s["weights_out"])

@@ -23,6 +23,16 @@ cache for generated tokens.
     dq, dkv, dk_rope = mla_bwd(q, kv, k_rope, o, lse, d_o, ...)
     mla_cache_append(latent, k_rope, cache, page_table, cache_lens)
     o, lse = mla_step(q_latent, q_rope, cache, page_table, seq_lens, scale)
+
+A smaller cache for it (include/kda_mla_cache.h): latents in 4 bits, and the
+eviction of the rows that attention has least use for, in either form.
+
+    cache = mla_cache_mx(n_pages, page_size, latent, rope, dtype)
+    mla_cache_append_mx(latent, k_rope, cache, page_table, cache_lens)
+    latent, k_rope = mla_cache_read_mx(cache, page_table, cu_seqlens, total, latent, dtype)
+    o, lse = mla_step_mx(q_latent, q_rope, cache, page_table, seq_lens, scale)
+    weights = mla_weigh(q_latent, q_rope, cache, page_table, seq_lens, lse, scale, weights)
+    page_table, seq_lens, weights = mla_evict(cache, page_table, seq_lens, weights, keep)
 """
 from __future__ import annotations
 
@@ -132,6 +142,23 @@ def load_library(path: str = LIB_PATH):
     lib.kda_mla_step_workspace_bytes.restype = Z
     lib.kda_mla_step.argtypes = [P, I64, I64, I64, P, I64, I64, I64, P, P, P] + [I32] * 8 + [F, D, P, Z, P, P, P]
     lib.kda_mla_step.restype = ctypes.c_int
+    lib.kda_mla_mx_row_bytes.argtypes = [I32, I32, D]
+    lib.kda_mla_mx_row_bytes.restype = Z
+    lib.kda_mla_cache_append_mx.argtypes = lib.kda_mla_cache_append.argtypes
+    lib.kda_mla_cache_append_mx.restype = ctypes.c_int
+    lib.kda_mla_cache_read_mx.argtypes = [P] * 4 + [I32] * 7 + [D, I32, P, P, P]
+    lib.kda_mla_cache_read_mx.restype = ctypes.c_int
+    lib.kda_mla_step_mx_workspace_bytes.argtypes = lib.kda_mla_step_workspace_bytes.argtypes
+    lib.kda_mla_step_mx_workspace_bytes.restype = Z
+    lib.kda_mla_step_mx.argtypes = lib.kda_mla_step.argtypes
+    lib.kda_mla_step_mx.restype = ctypes.c_int
+    lib.kda_mla_weigh.argtypes = ([P, I64, I64, I64, P, I64, I64, I64, P, P, P, P, P, I32, F] + [I32] * 8 +
+                                  [F, D, I32, P, P])
+    lib.kda_mla_weigh.restype = ctypes.c_int
+    lib.kda_mla_evict_workspace_bytes.argtypes = [I32] * 3
+    lib.kda_mla_evict_workspace_bytes.restype = Z
+    lib.kda_mla_evict.argtypes = [P] * 4 + [I32] * 9 + [D, I32, P, Z, P, P, P, P]
+    lib.kda_mla_evict.restype = ctypes.c_int
     lib.kda_status_string.argtypes = [ctypes.c_int]
     lib.kda_status_string.restype = ctypes.c_char_p
     lib.kda_last_error_message.argtypes = []
@@ -966,19 +993,24 @@ def _mla_cache(cache, page_table, lens, name, dt, dev, N):
     n_pages, page_size, D = cache.shape
     _need(cache, "cache", (n_pages, page_size, D), dt, dev)
     _need(page_table, "page_table", (N, page_table.shape[1]), torch.int32, dev)
-    _need(lens, name, (N,), torch.int32, dev)
+    if name is not None:
+        _need(lens, name, (N,), torch.int32, dev)
     return n_pages, page_size, page_table.shape[1], D
 
 
-def mla_cache_append(latent, k_rope, cache, page_table, cache_lens, cu_seqlens=None):
-    """Write new tokens into the paged cache of latents (kda_mla_cache_append).
+def _mla_rows(cache, page_table, lens, name, dt, dev, N, Dc, Dr, mx, what):
+    """Checks a cache of either form against rows of Dc + Dr channels."""
+    n_pages, page_size, max_pages, D = _mla_cache(cache, page_table, lens, name, torch.uint8 if mx else dt, dev, N)
+    if not mx:
+        if D != Dc + Dr:
+            raise ValueError(f"cache rows have {D} channels, {what} {Dc + Dr}")
+    elif D != mla_mx_row_bytes(Dc, Dr, dt):
+        raise ValueError(f"cache rows have {D} bytes, {what} of {Dc} + {Dr} channels in {dt} "
+                         f"{mla_mx_row_bytes(Dc, Dr, dt)}")
+    return n_pages, page_size, max_pages
 
-    latent [B,T,Dc], k_rope [B,T,Dr] or None (rows may be strided); cache
-    [n_pages,page_size,Dc+Dr]; page_table int32 [N,max_pages]; cache_lens int32
-    [N], the lengths before the call (negative: padding row), not changed;
-    cu_seqlens int32 [N+1] (B must be 1) or None (N = B). Pages that do not
-    exist are reported by ``device_check``."""
-    lib = load_library()
+
+def _mla_append(fn, mx, latent, k_rope, cache, page_table, cache_lens, cu_seqlens):
     if latent.dim() != 3:
         raise ValueError("latent must be [B,T,Dc]")
     B, T, Dc = latent.shape
@@ -997,15 +1029,25 @@ def mla_cache_append(latent, k_rope, cache, page_table, cache_lens, cu_seqlens=N
             raise ValueError("cu_seqlens must be 1-D")
         N = cu_seqlens.numel() - 1
         _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
-    n_pages, page_size, max_pages, D = _mla_cache(cache, page_table, cache_lens, "cache_lens", dt, dev, N)
-    if D != Dc + Dr:
-        raise ValueError(f"cache rows have {D} channels, latent and k_rope {Dc + Dr}")
+    n_pages, page_size, max_pages = _mla_rows(cache, page_table, cache_lens, "cache_lens", dt, dev, N, Dc, Dr, mx,
+                                              "latent and k_rope")
     lrow, lbatch = _steps(latent, 1, 0)
     krow, kbatch = _steps(k_rope, 1, 0)
     with _on(dev):
-        _check(lib.kda_mla_cache_append(_ptr(latent), lrow, lbatch, _ptr(k_rope), krow, kbatch, _ptr(cache),
-                                        _ptr(page_table), _ptr(cache_lens), _ptr(cu_seqlens), n_pages, page_size,
-                                        max_pages, B, T, Dc, Dr, N, _DTYPES[dt], _stream(dev)))
+        _check(fn(_ptr(latent), lrow, lbatch, _ptr(k_rope), krow, kbatch, _ptr(cache), _ptr(page_table),
+                  _ptr(cache_lens), _ptr(cu_seqlens), n_pages, page_size, max_pages, B, T, Dc, Dr, N, _DTYPES[dt],
+                  _stream(dev)))
+
+
+def mla_cache_append(latent, k_rope, cache, page_table, cache_lens, cu_seqlens=None):
+    """Write new tokens into the paged cache of latents (kda_mla_cache_append).
+
+    latent [B,T,Dc], k_rope [B,T,Dr] or None (rows may be strided); cache
+    [n_pages,page_size,Dc+Dr]; page_table int32 [N,max_pages]; cache_lens int32
+    [N], the lengths before the call (negative: padding row), not changed;
+    cu_seqlens int32 [N+1] (B must be 1) or None (N = B). Pages that do not
+    exist are reported by ``device_check``."""
+    _mla_append(load_library().kda_mla_cache_append, False, latent, k_rope, cache, page_table, cache_lens, cu_seqlens)
 
 
 def mla_step_workspace_bytes(Nb, Tq, H, Dc, page_size, max_pages, dtype):
@@ -1013,17 +1055,7 @@ def mla_step_workspace_bytes(Nb, Tq, H, Dc, page_size, max_pages, dtype):
     return int(load_library().kda_mla_step_workspace_bytes(Nb, Tq, H, Dc, page_size, max_pages, _DTYPES[dtype]))
 
 
-def mla_step(q_latent, q_rope, cache, page_table, seq_lens, scale, out=None, lse=None, workspace=None):
-    """Latent attention of Tq new tokens per row over the paged cache, absorbed
-    form (kda_mla_step).
-
-    q_latent [Nb,Tq,H,Dc], q_rope [Nb,Tq,H,Dr] or None, any strides with
-    contiguous channels; cache [n_pages,page_size,Dc+Dr], which holds the new
-    tokens already; page_table int32 [Nb,max_pages]; seq_lens int32 [Nb] with
-    the new tokens counted (<= 0: padding row). scale: of the expanded head, 1 /
-    sqrt(Dn + Dr). Returns (o [Nb,Tq,H,Dc] in latent space, lse [Nb,Tq,H]
-    float32). Pages that do not exist are reported by ``device_check``."""
-    lib = load_library()
+def _mla_queries(q_latent, q_rope):
     if q_latent.dim() != 4:
         raise ValueError("q_latent must be [Nb,Tq,H,Dc]")
     Nb, Tq, H, Dc = q_latent.shape
@@ -1036,9 +1068,13 @@ def mla_step(q_latent, q_rope, cache, page_table, seq_lens, scale, out=None, lse
     _need_rows(q_latent, "q_latent", (Nb, Tq, H, Dc), dt, dev)
     if q_rope is not None:
         _need_rows(q_rope, "q_rope", (Nb, Tq, H, Dr), dt, dev)
-    n_pages, page_size, max_pages, D = _mla_cache(cache, page_table, seq_lens, "seq_lens", dt, dev, Nb)
-    if D != Dc + Dr:
-        raise ValueError(f"cache rows have {D} channels, q_latent and q_rope {Dc + Dr}")
+    return Nb, Tq, H, Dc, Dr, dt, dev
+
+
+def _mla_step(fn, workspace_bytes, mx, q_latent, q_rope, cache, page_table, seq_lens, scale, out, lse, workspace):
+    Nb, Tq, H, Dc, Dr, dt, dev = _mla_queries(q_latent, q_rope)
+    n_pages, page_size, max_pages = _mla_rows(cache, page_table, seq_lens, "seq_lens", dt, dev, Nb, Dc, Dr, mx,
+                                              "q_latent and q_rope")
     if out is None:
         out = torch.empty((Nb, Tq, H, Dc), dtype=dt, device=dev)
     else:
@@ -1047,13 +1083,200 @@ def mla_step(q_latent, q_rope, cache, page_table, seq_lens, scale, out=None, lse
         lse = torch.empty((Nb, Tq, H), dtype=torch.float32, device=dev)
     else:
         _need(lse, "lse", (Nb, Tq, H), torch.float32, dev)
-    workspace = _workspace(workspace, mla_step_workspace_bytes(Nb, Tq, H, Dc, page_size, max_pages, dt), dev)
+    workspace = _workspace(workspace, workspace_bytes(Nb, Tq, H, Dc, page_size, max_pages, dt), dev)
     with _on(dev):
-        _check(lib.kda_mla_step(_ptr(q_latent), *_steps(q_latent, 0, 1, 2), _ptr(q_rope), *_steps(q_rope, 0, 1, 2),
-                                _ptr(cache), _ptr(page_table), _ptr(seq_lens), n_pages, page_size, max_pages, Nb, Tq,
-                                H, Dc, Dr, float(scale), _DTYPES[dt], _ptr(workspace), workspace.numel(), _ptr(out),
-                                _ptr(lse), _stream(dev)))
+        _check(fn(_ptr(q_latent), *_steps(q_latent, 0, 1, 2), _ptr(q_rope), *_steps(q_rope, 0, 1, 2), _ptr(cache),
+                  _ptr(page_table), _ptr(seq_lens), n_pages, page_size, max_pages, Nb, Tq, H, Dc, Dr, float(scale),
+                  _DTYPES[dt], _ptr(workspace), workspace.numel(), _ptr(out), _ptr(lse), _stream(dev)))
     return out, lse
+
+
+def mla_step(q_latent, q_rope, cache, page_table, seq_lens, scale, out=None, lse=None, workspace=None):
+    """Latent attention of Tq new tokens per row over the paged cache, absorbed
+    form (kda_mla_step).
+
+    q_latent [Nb,Tq,H,Dc], q_rope [Nb,Tq,H,Dr] or None, any strides with
+    contiguous channels; cache [n_pages,page_size,Dc+Dr], which holds the new
+    tokens already; page_table int32 [Nb,max_pages]; seq_lens int32 [Nb] with
+    the new tokens counted (<= 0: padding row). scale: of the expanded head, 1 /
+    sqrt(Dn + Dr). Returns (o [Nb,Tq,H,Dc] in latent space, lse [Nb,Tq,H]
+    float32). Pages that do not exist are reported by ``device_check``."""
+    return _mla_step(load_library().kda_mla_step, mla_step_workspace_bytes, False, q_latent, q_rope, cache, page_table,
+                     seq_lens, scale, out, lse, workspace)
+
+
+def mla_mx_row_bytes(latent, rope, dtype):
+    """Bytes of a row of the 4-bit cache (0 for sizes that are not supported)."""
+    key = (latent, rope, dtype)
+    n = _mx_rows.get(key)
+    if n is None:
+        n = int(load_library().kda_mla_mx_row_bytes(latent, rope, _DTYPES[dtype]))
+        if n:
+            _mx_rows[key] = n
+    return n
+
+
+_mx_rows = {}
+
+
+def mla_cache_mx(n_pages, page_size, latent, rope, dtype, device="cuda"):
+    """A 4-bit cache of n_pages pages for latents of `latent` channels and shared
+    key parts of `rope` (0: none) in dtype, whose rows are all zeros: uint8
+    [n_pages,page_size,row bytes]. The bytes of a page are not those of its rows
+    one after the other: all rows' codes come first, then their scales, then
+    their shared parts (include/kda_mla_cache.h)."""
+    row = mla_mx_row_bytes(latent, rope, dtype) if dtype in _DTYPES else 0
+    if not row:
+        raise ValueError(f"no 4-bit cache for {latent} + {rope} channels in {dtype}")
+    return torch.zeros((n_pages, page_size, row), dtype=torch.uint8, device=device)
+
+
+def mla_cache_append_mx(latent, k_rope, cache, page_table, cache_lens, cu_seqlens=None):
+    """Round new tokens to 4 bits and write them into the paged cache
+    (kda_mla_cache_append_mx): ``mla_cache_append`` for a cache as
+    ``mla_cache_mx`` makes it. The shared key parts keep their dtype."""
+    _mla_append(load_library().kda_mla_cache_append_mx, True, latent, k_rope, cache, page_table, cache_lens, cu_seqlens)
+
+
+def mla_cache_read_mx(cache, page_table, cu_seqlens, total, latent, dtype, starts=None, out=None):
+    """Rows of the 4-bit cache, packed (kda_mla_cache_read_mx).
+
+    cu_seqlens int32 [N+1]: rows cu_seqlens[n] .. of the outputs are sequence
+    n's rows from starts[n] (int32 [N]; None: 0) on; total: rows of the outputs
+    (the host's cu_seqlens[-1], or more); latent: channels of a latent. Returns
+    (latent [1,total,latent], k_rope [1,total,rope] or None) in dtype, as the
+    up-projection and ``mla_fwd`` take them. Rows behind the last sequence are
+    zeros, and left as they were where ``out`` = (latent, k_rope or None) is
+    given. Rows that do not exist are zeros and reported by ``device_check``."""
+    lib = load_library()
+    if dtype not in _DTYPES:
+        raise TypeError(f"unsupported dtype {dtype}")
+    dev = cache.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a GPU")
+    if cu_seqlens.dim() != 1 or cu_seqlens.numel() < 2:
+        raise ValueError("cu_seqlens must be 1-D with an entry more than there are sequences")
+    N = cu_seqlens.numel() - 1
+    if cache.dim() != 3 or page_table.dim() != 2:
+        raise ValueError("cache must be [n_pages,page_size,row bytes] and page_table [N,max_pages]")
+    _need(cu_seqlens, "cu_seqlens", (N + 1,), torch.int32, dev)
+    rope = 64 if cache.shape[2] > mla_mx_row_bytes(latent, 0, dtype) else 0
+    n_pages, page_size, max_pages = _mla_rows(cache, page_table, starts, None if starts is None else "starts", dtype,
+                                              dev, N, latent, rope, True, "latents")
+    if out is None:
+        x = torch.empty((1, total, latent), dtype=dtype, device=dev)
+        r = torch.empty((1, total, rope), dtype=dtype, device=dev) if rope else None
+    else:
+        x, r = out
+        _need(x, "out[0]", (1, total, latent), dtype, dev)
+        if rope:
+            _need(r, "out[1]", (1, total, rope), dtype, dev)
+        elif r is not None:
+            raise ValueError("out[1] must be None: the cache has no shared key part")
+    with _on(dev):
+        _check(lib.kda_mla_cache_read_mx(_ptr(cache), _ptr(page_table), _ptr(starts), _ptr(cu_seqlens), n_pages,
+                                         page_size, max_pages, total, latent, rope, N, _DTYPES[dtype],
+                                         int(out is None), _ptr(x), _ptr(r), _stream(dev)))
+    return x, r
+
+
+def mla_step_mx_workspace_bytes(Nb, Tq, H, Dc, page_size, max_pages, dtype):
+    """Bytes of workspace kda_mla_step_mx needs."""
+    return int(load_library().kda_mla_step_mx_workspace_bytes(Nb, Tq, H, Dc, page_size, max_pages, _DTYPES[dtype]))
+
+
+def mla_step_mx(q_latent, q_rope, cache, page_table, seq_lens, scale, out=None, lse=None, workspace=None):
+    """``mla_step`` over a 4-bit cache (kda_mla_step_mx): the same arguments and
+    results, cache as ``mla_cache_mx`` makes it for the queries' dtype."""
+    return _mla_step(load_library().kda_mla_step_mx, mla_step_mx_workspace_bytes, True, q_latent, q_rope, cache,
+                     page_table, seq_lens, scale, out, lse, workspace)
+
+
+def _rows_i32(n):
+    """A number of rows as the library takes it: more than 2^31 - 1 mean the same."""
+    return min(int(n), 0x7fffffff)
+
+
+def mla_weigh(q_latent, q_rope, cache, page_table, seq_lens, lse, scale, weights, fresh=None, decay=1.0, out=None):
+    """Add to the cached rows' weights the attention that new tokens pay them
+    (kda_mla_weigh): weights[n][j] = decay * weights[n][j] + the sum over the
+    tokens and heads of their softmax's weight of row j.
+
+    q_latent, q_rope, page_table, seq_lens, scale: as ``mla_step`` had them, lse
+    its result; cache of either form (uint8: 4 bits); weights float32 [Nb,
+    max_pages * page_size]. fresh: so many of each sequence's last rows have no
+    weight yet (None: the new tokens; after a prefill: the prompt's rows, or
+    more). Changed in place, or written to ``out``; rows from seq_lens[n] on are
+    not touched. Returns the result."""
+    lib = load_library()
+    Nb, Tq, H, Dc, Dr, dt, dev = _mla_queries(q_latent, q_rope)
+    mx = cache.dtype == torch.uint8
+    n_pages, page_size, max_pages = _mla_rows(cache, page_table, seq_lens, "seq_lens", dt, dev, Nb, Dc, Dr, mx,
+                                              "q_latent and q_rope")
+    _need(lse, "lse", (Nb, Tq, H), torch.float32, dev)
+    _need(weights, "weights", (Nb, max_pages * page_size), torch.float32, dev)
+    if out is None:
+        out = weights
+    else:
+        _need(out, "out", weights.shape, torch.float32, dev)
+    with _on(dev):
+        _check(lib.kda_mla_weigh(_ptr(q_latent), *_steps(q_latent, 0, 1, 2), _ptr(q_rope), *_steps(q_rope, 0, 1, 2),
+                                 _ptr(cache), _ptr(page_table), _ptr(seq_lens), _ptr(lse), _ptr(weights),
+                                 Tq if fresh is None else _rows_i32(fresh), float(decay), n_pages, page_size, max_pages, Nb,
+                                 Tq, H, Dc, Dr, float(scale), _DTYPES[dt], int(mx), _ptr(out), _stream(dev)))
+    return out
+
+
+def mla_evict_workspace_bytes(Nb, page_size, max_pages):
+    """Bytes of workspace kda_mla_evict needs."""
+    return int(load_library().kda_mla_evict_workspace_bytes(Nb, page_size, max_pages))
+
+
+# rows of a 4-bit cache by their bytes: (latent, rope, dtype); without a shared part the dtype does not matter
+_MX_ROWS = {136: (256, 0, KDA_BF16), 264: (256, 64, KDA_BF16), 392: (256, 64, KDA_F32), 272: (512, 0, KDA_BF16),
+            400: (512, 64, KDA_BF16), 528: (512, 64, KDA_F32)}
+
+
+def mla_evict(cache, page_table, seq_lens, weights, keep, first=0, recent=0, out=None, workspace=None):
+    """Evict whole pages of the least-weighted rows from sequences of more than
+    `keep` rows, at most down to it (kda_mla_evict).
+
+    cache of either form, changed in place; page_table int32 [Nb,max_pages],
+    seq_lens int32 [Nb], weights float32 [Nb, max_pages * page_size], changed in
+    place or written to ``out`` = (page_table, seq_lens, weights). The pages of the
+    first `first` and last `recent` rows stay as they are; they alone may be shared by
+    sequences. Emptied pages stand in the page table behind those in use. Returns
+    (page_table, seq_lens, weights). Sequences with missing pages stay as they are
+    and are reported by ``device_check``."""
+    lib = load_library()
+    dev = cache.device
+    if dev.type != "cuda":
+        raise ValueError("inputs must be on a GPU")
+    Nb = seq_lens.numel()
+    n_pages, page_size, max_pages, D = _mla_cache(cache, page_table, seq_lens, "seq_lens", cache.dtype, dev, Nb)
+    _need(weights, "weights", (Nb, max_pages * page_size), torch.float32, dev)
+    if cache.dtype == torch.uint8:
+        if D not in _MX_ROWS:
+            raise ValueError(f"cache rows of {D} bytes are not those of a 4-bit cache")
+        Dc, Dr, dt = _MX_ROWS[D]
+    elif cache.dtype in _DTYPES:
+        Dr, dt = 64 if D % 256 else 0, _DTYPES[cache.dtype]
+        Dc = D - Dr
+    else:
+        raise TypeError(f"unsupported dtype {cache.dtype}")
+    if out is None:
+        out = page_table, seq_lens, weights
+    else:
+        _need(out[0], "out[0]", page_table.shape, torch.int32, dev)
+        _need(out[1], "out[1]", seq_lens.shape, torch.int32, dev)
+        _need(out[2], "out[2]", weights.shape, torch.float32, dev)
+    workspace = _workspace(workspace, mla_evict_workspace_bytes(Nb, page_size, max_pages), dev)
+    with _on(dev):
+        _check(lib.kda_mla_evict(_ptr(cache), _ptr(page_table), _ptr(seq_lens), _ptr(weights), _rows_i32(keep),
+                                 _rows_i32(first), _rows_i32(recent), n_pages, page_size, max_pages, Nb, Dc, Dr, dt,
+                                 int(cache.dtype == torch.uint8), _ptr(workspace), workspace.numel(), _ptr(out[0]),
+                                 _ptr(out[1]), _ptr(out[2]), _stream(dev)))
+    return tuple(out)
 
 
 def device_check(device=None):

@@ -17,7 +17,8 @@ HIPCC = os.environ.get("HIPCC", "/opt/rocm/bin/hipcc")
 
 SOURCES = ["kda_api.hip", "chunk_mfma.hip", "chunk_generic.hip", "chunk_bwd.hip", "recurrent_step.hip",
            "short_conv.hip", "split.hip", "prologue_bwd.hip", "mla_api.hip", "mla_fwd.hip", "mla_bwd.hip",
-           "mla_dkv_bf16.hip", "mla_step.hip"]
+           "mla_dkv_bf16.hip", "mla_step.hip", "mla_cache_api.hip", "mla_mx_rows.hip", "mla_step_mx.hip", "mla_weigh.hip",
+           "mla_evict.hip"]
 CFLAGS = [
     "--offload-arch=gfx950", "-O3", "-std=c++17", "-fPIC", "-Wall", "-Wno-unused-function",
     # no packed-fp32 instructions in any generated code

@@ -295,10 +295,53 @@ struct MlaAppendArgs {
     bool bf16;
 };
 
+struct MlaReadArgs {            // rows out of a 4-bit cache (kda_mla_cache_read_mx)
+    const void* cache;
+    const int32_t* table;       // [N,max_pages]
+    const int32_t* starts;      // [N] or nullptr
+    const int32_t* cu;          // [N+1]
+    void* latent;               // [T,Dc]
+    void* rope;                 // [T,Dr] or nullptr when Dr = 0
+    unsigned int* status;
+    int32_t n_pages, page_shift, max_pages, T, Dc, Dr, N;
+    bool bf16, zero_rest;
+};
+struct MlaWeighArgs {           // kda_mla_weigh
+    MlaStepArgs s;              // queries, cache, lengths (no output, no workspace)
+    const float* lse;           // [Nb,Tq,H]
+    const float* w_in;          // [Nb,max_pages * page_size]
+    float* w_out;
+    int32_t fresh;
+    float decay;
+    bool mx;
+};
+struct MlaEvictArgs {           // kda_mla_evict
+    char* cache;
+    const int32_t* table;       // [Nb,max_pages]
+    const int32_t* lens;
+    const float* w_in;          // [Nb,max_pages * page_size]
+    int32_t* table_out;
+    int32_t* lens_out;
+    float* w_out;
+    int32_t* moves;             // workspace: [Nb] numbers of moves, then [Nb][2][moves at most] destinations and sources
+    unsigned int* status;
+    int32_t n_pages, page_shift, max_pages, Nb, keep, first, recent;
+    // a row's pieces in a page: `units` of 16 bytes, of which those behind the first
+    // `codes` (4-bit form) are a row's scale bytes, then its shared part
+    int32_t units, codes, scale_bytes, rope;
+};
+
 // Fills the split of a decode call and returns its workspace in bytes.
 size_t mla_step_plan(MlaStepArgs& a);
 hipError_t launch_mla_step(const MlaStepArgs& a, hipStream_t stream);
 hipError_t launch_mla_append(const MlaAppendArgs& a, hipStream_t stream);
+hipError_t launch_mla_step_mx(const MlaStepArgs& a, hipStream_t stream);       // the same over a 4-bit cache
+size_t mla_step_mx_plan(MlaStepArgs& a);
+hipError_t launch_mla_append_mx(const MlaAppendArgs& a, hipStream_t stream);
+hipError_t launch_mla_read_mx(const MlaReadArgs& a, hipStream_t stream);
+hipError_t launch_mla_weigh(const MlaWeighArgs& a, hipStream_t stream);
+int64_t mla_evict_moves(int32_t page_shift, int32_t max_pages);                // of a sequence, at most
+hipError_t launch_mla_evict(const MlaEvictArgs& a, hipStream_t stream);
 hipError_t launch_mla_fwd(const MlaArgs& a, hipStream_t stream);
 hipError_t launch_mla_bwd(const MlaArgs& a, hipStream_t stream);
 hipError_t launch_mla_dkv_bf16(const MlaArgs& a, hipStream_t stream);   // its second kernel

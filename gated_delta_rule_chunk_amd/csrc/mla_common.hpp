@@ -47,6 +47,16 @@ __device__ __forceinline__ f32x16 mma(f32x8 a, f32x8 b, f32x16 c) {
     for (int j = 0; j < 8; ++j) c = __builtin_amdgcn_mfma_f32_32x32x2f32(a[j], b[j], c, 0, 0, 0);
     return c;
 }
+// Waits until the matrix instructions before it have written x (and y): up to 20
+// wait states. The compiler counts them itself, but not along a branch taken
+// right behind the last of them (seen: two states where eight are needed, and
+// the last product missing from the sum). The asm reads nothing.
+template <class V> __device__ __forceinline__ void settle(V& x) {
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 3" : "+v"(x));
+}
+template <class V> __device__ __forceinline__ void settle(V& x, V& y) {
+    asm volatile("s_nop 7\n\ts_nop 7\n\ts_nop 3" : "+v"(x), "+v"(y));
+}
 __device__ __forceinline__ f32x16 zero16() {
     f32x16 z;
 #pragma unroll

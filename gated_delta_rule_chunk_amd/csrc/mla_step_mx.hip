@@ -1,0 +1,329 @@
+// Latent attention, absorbed form, over a cache that holds the latents in 4 bits
+// (include/kda_mla_cache.h): s = scale (q_latent . c + q_rope . r), p = softmax s,
+// o = sum p c.
+//
+// As in mla_step.hip the tiles of 32 cache rows of all sequences form one list,
+// cut into equal parts by the lengths on the device, and a second kernel joins
+// the parts. A tile's codes come to registers a tile ahead, 32 channels a
+// thread, and are written to LDS as T. Four waves share a block of 32 rows of
+// queries: each forms the scores of 16 rows and 16 keys, the two that share
+// rows agree on the running maximum, and each multiplies the probabilities of
+// all 32 rows with a quarter of the columns. So neither queries, scores nor outputs
+// (Dc / 8 registers) take more than a third of a SIMD's registers, and three
+// blocks (96 rows) leave each SIMD three waves.
+#include "mla_mx.hpp"
+#include "mla_step.hpp"
+
+namespace kda {
+namespace {
+
+// blocks of 32 rows of queries a workgroup, at most (float32: its queries take twice the registers)
+template <class T> constexpr int kMostBlocks = sizeof(T) == 2 ? 3 : 2;
+
+template <class T, int DC, int DR, int RB>
+__global__ __launch_bounds__(256 * RB, RB) void mla_mx_step_kernel(MlaStepArgs a) {
+    constexpr int D = DC + DR, RC = D / kChunk<T>, NS = D / 32, ND = DC / 64, NT = 256 * RB;
+    constexpr int NB = DC / 32, RR = DR / kChunk<T>;          // blocks of 32 channels, 16-byte chunks of the shared part
+    constexpr int CI = (kTile * NB + NT - 1) / NT, RI = (kTile * RR + NT - 1) / NT;     // of them a thread
+    __shared__ __attribute__((aligned(1024))) char smem[2][kTile * RC * 16];
+    __shared__ __attribute__((aligned(32))) T probs[RB][2][64][8];
+    __shared__ float tops[RB][2][2][16], factor[RB][2][16];
+    const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
+    const int rb = w >> 2, quarter = w & 3, rh = w & 1, kh = quarter >> 1;
+    const int group = blockIdx.x % a.groups, part = blockIdx.x / a.groups;
+    Scan sq = scan_tiles(a, 0, lane);
+    int total = sq.all();
+    for (int b = 64; b < a.Nb; b += 64) total += scan_tiles(a, b, lane).all();
+    const int per = part_tiles(a, total);
+    int at = part * per;                                         // next tile of the list
+    const int end = total - at < per ? total : at + per;
+    if (at >= total) return;
+    const int M = a.Tq * a.H;
+    const float c = a.scale * kLog2e;
+    const int ps = a.page_shift;
+    const int64_t page_bytes = (int64_t)mx_row_bytes(DC, DR, sizeof(T)) << ps;
+
+    int b0 = 0, before = 0;                                      // sq's first sequence, tiles before it
+    while (at < end) {
+        while (at >= before + sq.all()) {
+            before += sq.all();
+            b0 += 64;
+            sq = scan_tiles(a, b0, lane);
+        }
+        const int l = __ffsll((unsigned long long)__ballot(before + sq.sum > at)) - 1;
+        const int b = b0 + l;
+        const int tiles = __builtin_amdgcn_readlane(sq.cnt, l), len = __builtin_amdgcn_readlane(sq.len, l);
+        const int rows = __builtin_amdgcn_readlane(sq.rows, l);
+        const int first = before + __builtin_amdgcn_readlane(sq.sum, l) - tiles;    // the sequence's place in the list
+        const int t0 = at - first, t1 = end - first < tiles ? end - first : tiles;
+        at = first + t1;
+        if (t0 == 0 && group == 0 && tid == 0 && len > rows) atomicAdd(a.status, 1u);
+
+        // queries: row 32 (RB group + rb) + 16 rh + n of the (token, head) pairs
+        const int row = ((group * RB + rb) * 2 + rh) * 16 + (lane & 15), mrow = row < M ? row : M - 1;
+        const int tok = mrow / a.H, head = mrow - tok * a.H;
+        const T* qlp = static_cast<const T*>(a.ql) + b * a.ql_b + tok * a.ql_t + head * a.ql_h + 8 * (lane >> 4);
+        const T* qrp = static_cast<const T*>(a.qr) + b * a.qr_b + tok * a.qr_t + head * a.qr_h + 8 * (lane >> 4);
+        f32x4 acc[2][ND];                                         // of the block's two sets of 16 rows
+#pragma unroll
+        for (int d = 0; d < ND; ++d) acc[0][d] = acc[1][d] = f32x4{0.f, 0.f, 0.f, 0.f};
+        float m = -INFINITY, lsum = 0.f;
+
+        // Page table entries of 64 pages, one per lane; -1 for no such page or one
+        // past the rows. A tile's halves lie in one page or, where pages have
+        // 16 rows, in an even one and the next: of the same 64.
+        const int32_t* table = a.table + (int64_t)b * a.max_pages;
+        int pbase = -64, pages = 0;
+        auto entry = [&](int p) {
+            const int i = p + lane;
+            return i < a.max_pages && (int64_t)i << ps < rows ? table[i] : 0;
+        };
+        auto keep = [&](int p, int e) {
+            pbase = p;
+            const int64_t r = (int64_t)(p + lane) << ps;
+            if (e < 0 || e >= a.n_pages) e = -1;
+            // counted once: where the page's first row is this part's
+            const uint64_t bad = __ballot(e < 0 && r >= t0 * kTile && r < (int64_t)t1 * kTile);
+            if (bad && group == 0 && tid == 0) atomicAdd(a.status, (unsigned)__popcll(bad));
+            pages = r < rows ? e : -1;
+        };
+        // the first entries and the queries are under way together
+        const int p0 = t0 * kTile >> ps, e = entry(p0);
+        Frag<T> qf[NS];
+#pragma unroll
+        for (int s = 0; s < NS; ++s) qf[s] = s < DC / 32 ? load8(qlp + 32 * s) : load8(qrp + 32 * s - DC);
+        keep(p0, e);
+
+        // A tile on its way: this thread's blocks and chunks. Rows past the length
+        // and of missing pages are zeros: hidden rows' weights are 0, but what they multiply has to be finite.
+        u32x4 codes[CI], shared_part[RI ? RI : 1];
+        uint32_t scale[CI];
+        int have = 0;
+        auto fetch = [&](int t) {
+            const int k0 = t * kTile, p = k0 >> ps;
+            if (p >= pbase + 64) keep(p, entry(p));
+            const int e0 = __builtin_amdgcn_readlane(pages, p - pbase);
+            const int e1 = __builtin_amdgcn_readlane(pages, ((k0 + 16) >> ps) - pbase);
+            const int mask = (1 << ps) - 1;
+            const char* const lo = static_cast<const char*>(a.cache) + e0 * page_bytes;
+            const char* const hi = static_cast<const char*>(a.cache) + e1 * page_bytes;
+            have = (e0 >= 0 ? 1 : 0) | (e1 >= 0 ? 2 : 0);
+#pragma unroll
+            for (int i = 0; i < CI; ++i) {
+                const int x = i * NT + tid, r = x / NB, blk = x % NB;
+                codes[i] = u32x4{0, 0, 0, 0};
+                scale[i] = 0;
+                if (r < kTile && k0 + r < rows && (have >> (r >> 4) & 1)) {
+                    const char* const page = r >> 4 ? hi : lo;
+                    const int64_t pr = (k0 + r) & mask;
+                    codes[i] = *reinterpret_cast<const u32x4*>(page + pr * (DC / 2) + blk * 16);
+                    scale[i] = *reinterpret_cast<const uint8_t*>(page + ((int64_t)(DC / 2) << ps) + pr * NB + blk);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                const int x = i * NT + tid, r = x / (RR ? RR : 1), ch = x % (RR ? RR : 1);
+                shared_part[i] = u32x4{0, 0, 0, 0};
+                if (r < kTile && k0 + r < rows && (have >> (r >> 4) & 1))
+                    shared_part[i] = *reinterpret_cast<const u32x4*>(
+                        (r >> 4 ? hi : lo) + ((int64_t)(DC / 2 + NB) << ps) + ((int64_t)((k0 + r) & mask) * RR + ch) * 16);
+            }
+        };
+        auto put = [&](char* to) {
+#pragma unroll
+            for (int i = 0; i < CI; ++i) {
+                const int x = i * NT + tid, r = x / NB, blk = x % NB, sw = swizzle16<T, RC>(r);
+                if (kTile * NB % NT && r >= kTile) break;
+                const MxScale f(scale[i]);
+                char* const p = to + r * (RC * 16);
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    if constexpr (sizeof(T) == 2) {
+                        *reinterpret_cast<bf16x8*>(p + (((4 * blk + j) ^ sw) << 4)) = f.bf16(codes[i][j]);
+                    } else {
+                        const f32x8 v = f.f32(codes[i][j]);
+                        *reinterpret_cast<f32x4*>(p + (((8 * blk + 2 * j) ^ sw) << 4)) = f32x4{v[0], v[1], v[2], v[3]};
+                        *reinterpret_cast<f32x4*>(p + (((8 * blk + 2 * j + 1) ^ sw) << 4)) = f32x4{v[4], v[5], v[6], v[7]};
+                    }
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < RI; ++i) {
+                const int x = i * NT + tid, r = x / (RR ? RR : 1), ch = x % (RR ? RR : 1);
+                if (kTile * RR % NT && r >= kTile) break;
+                *reinterpret_cast<u32x4*>(to + r * (RC * 16) + (((DC / kChunk<T> + ch) ^ swizzle16<T, RC>(r)) << 4)) =
+                    shared_part[i];
+            }
+        };
+        fetch(t0);
+        put(smem[0]);
+        int now = have;
+        if (t0 + 1 < t1) fetch(t0 + 1);
+        wait_lds();
+        wg_barrier();
+        for (int t = t0; t < t1; ++t) {
+            const char* const buf = smem[(t - t0) & 1];
+            int ln = lane;
+            asm volatile("" : "+v"(ln));                          // LDS addresses are formed here, not kept over the loop
+            const int g = ln >> 4;
+            f32x4 sc = {0.f, 0.f, 0.f, 0.f}, odd = sc;            // 16 keys, in two chains
+#pragma unroll
+            for (int s = 0; s < NS; ++s) {
+                const Frag<T> k = read_rows16<T, RC>(buf, 16 * kh + (ln & 15), s, g);
+                f32x4& y = s % 2 ? odd : sc;
+                y = mma16(k, qf[s], y);
+            }
+            settle(sc, odd);
+#pragma unroll
+            for (int r = 0; r < 4; ++r) sc[r] += odd[r];
+            // keys that this lane's token sees in the tile: the first lim + 1
+            const int k0 = t * kTile;
+            if (k0 + kTile > len - a.Tq + 1 || k0 + kTile > rows || now != 3) {
+                const int last = len - a.Tq + tok < rows - 1 ? len - a.Tq + tok : rows - 1, lim = last - k0 - 4 * g - 16 * kh;
+#pragma unroll
+                for (int r = 0; r < 4; ++r) sc[r] = r > lim || !(now >> kh & 1) ? -INFINITY : sc[r];
+            }
+            float mx = fmaxf(fmaxf(sc[0], sc[1]), fmaxf(sc[2], sc[3]));
+            mx = group_max(mx);
+            if (g == 0) tops[rb][rh][kh][ln] = mx;
+            wait_lds();
+            wg_barrier();
+            mx = fmaxf(mx, tops[rb][rh][kh ^ 1][ln & 15]);
+            // the running maximum moves as in mla_step.hip
+            float al = 1.f;
+            if ((mx - m) * c > 8.f) {
+                al = __builtin_amdgcn_exp2f((m - mx) * c);
+                lsum *= al;
+                m = mx;
+            }
+            const float m0 = m == -INFINITY ? 0.f : m;            // nothing seen yet: all terms are 0
+            T pf[4];
+#pragma unroll
+            for (int r = 0; r < 4; ++r) {
+                const float p = __builtin_amdgcn_exp2f((sc[r] - m0) * c);
+                lsum += p;
+                pf[r] = (T)p;                  // bf16: the one rounding of the probabilities, as operands
+            }
+#pragma unroll
+            for (int r = 0; r < 4; ++r) probs[rb][rh][ln][4 * kh + r] = pf[r];
+            if (g == 0 && kh == 0) factor[rb][rh][ln] = al;
+            // the next tile: its buffer's readers have passed the barrier
+            if (t + 1 < t1) {
+                put(smem[(t + 1 - t0) & 1]);
+                now = have;
+                if (t + 2 < t1) fetch(t + 2);
+            }
+            wait_lds();
+            wg_barrier();
+            Frag<T> p[2];
+            float f[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                p[s] = *reinterpret_cast<const Frag<T>*>(&probs[rb][s][ln][0]);
+                f[s] = factor[rb][s][ln & 15];
+            }
+            if (__any(f[0] != 1.f || f[1] != 1.f)) {
+#pragma unroll
+                for (int d = 0; d < ND; ++d)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) {
+                        acc[0][d][r] *= f[0];
+                        acc[1][d][r] *= f[1];
+                    }
+            }
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                const Frag<T> v = read_cols16<T, RC>(buf, quarter * (DC / 4) + 16 * d, ln);
+                acc[0][d] = mma16(v, p[0], acc[0][d]);
+                acc[1][d] = mma16(v, p[1], acc[1][d]);
+            }
+        }
+        // sums of both halves of the keys
+        float lt = group_sum(lsum);
+        wait_lds();
+        wg_barrier();
+        int ln = lane;
+        asm volatile("" : "+v"(ln));
+        const int g = ln >> 4, r0 = (group * RB + rb) * 32 + (ln & 15), r1 = r0 + 16;
+        if (g == 0) tops[rb][rh][kh][ln] = lt;
+        wait_lds();
+        wg_barrier();
+        lt = tops[rb][rh][0][ln & 15] + tops[rb][rh][1][ln & 15];
+        if (t0 == 0 && t1 == tiles) {
+            float inv[2];
+#pragma unroll
+            for (int s = 0; s < 2; ++s) {
+                const float x = tops[rb][s][0][ln & 15] + tops[rb][s][1][ln & 15];
+                inv[s] = x > 0.f ? 1.f / x : x == 0.f ? 0.f : x;  // no visible key: 0; NaN stays NaN
+            }
+            T* op = static_cast<T*>(a.o) + (int64_t)b * M * DC + quarter * (DC / 4) + 4 * g;
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                if (r0 < M) store4(op + (int64_t)r0 * DC + 16 * d, acc[0][d], inv[0]);
+                if (r1 < M) store4(op + (int64_t)r1 * DC + 16 * d, acc[1][d], inv[1]);
+            }
+            if (a.lse && row < M && g == 0 && kh == 0)
+                a.lse[(int64_t)b * M + row] =
+                    lt == 0.f ? -INFINITY : (m * c + __builtin_amdgcn_logf(lt)) * 0.6931471805599453f;
+        } else {
+            const int j = t0 > 0 ? 0 : 1;
+            float* const x0 = partial(a, group, part, j, 32 * rb + (ln & 15));
+            float* const x1 = partial(a, group, part, j, 32 * rb + 16 + (ln & 15));
+            if (g == 0 && kh == 0) {
+                float* const p = rh ? x1 : x0;
+                p[0] = m * c;
+                p[1] = lt;
+            }
+#pragma unroll
+            for (int d = 0; d < ND; ++d) {
+                store4(x0 + 4 + quarter * (DC / 4) + 16 * d + 4 * g, acc[0][d], 1.f);
+                store4(x1 + 4 + quarter * (DC / 4) + 16 * d + 4 * g, acc[1][d], 1.f);
+            }
+        }
+        wait_lds();
+        wg_barrier();                                             // the next sequence writes tops again
+    }
+}
+
+template <class T, int DC, int DR> hipError_t launch_mx(const MlaStepArgs& a, hipStream_t s) {
+    const dim3 grid((unsigned)(a.groups * a.parts));
+    if (a.waves == 2) mla_mx_step_kernel<T, DC, DR, 1><<<grid, 256, 0, s>>>(a);
+    else if (a.waves == 4) mla_mx_step_kernel<T, DC, DR, 2><<<grid, 512, 0, s>>>(a);
+    else if constexpr (kMostBlocks<T> > 2) mla_mx_step_kernel<T, DC, DR, 3><<<grid, 768, 0, s>>>(a);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    const int blocks = (a.Tq * a.H + a.join_rows - 1) / a.join_rows;
+    mla_step_join_kernel<T, DC><<<dim3((unsigned)((int64_t)a.Nb * blocks)), 256, 0, s>>>(a, blocks);
+    return hipGetLastError();
+}
+template <class T> hipError_t launch_mx_dims(const MlaStepArgs& a, hipStream_t s) {
+    if (a.Dc == 512) return a.Dr ? launch_mx<T, 512, 64>(a, s) : launch_mx<T, 512, 0>(a, s);
+    return a.Dr ? launch_mx<T, 256, 64>(a, s) : launch_mx<T, 256, 0>(a, s);
+}
+
+}  // namespace
+
+// The split over workgroups: blocks of 32 rows of queries spread evenly over as few
+// groups as hold them; a cache so short that there is a compute unit for each
+// tile and group gets more of them.
+size_t mla_step_mx_plan(MlaStepArgs& a) {
+    const int64_t rows = (int64_t)a.Tq * a.H, blocks = (rows + 31) / 32;
+    const int64_t most = (int64_t)a.Nb * ((((int64_t)a.max_pages << a.page_shift) + kTile - 1) / kTile);
+    int64_t per = a.bf16 ? kMostBlocks<__bf16> : kMostBlocks<float>;    // blocks a workgroup
+    while (per > 1 && (blocks + per - 2) / (per - 1) * most <= 256) --per;
+    a.groups = (int32_t)((blocks + per - 1) / per);
+    a.waves = (int32_t)((blocks + a.groups - 1) / a.groups) * 2;
+    int64_t parts = kMaxParts / a.groups;
+    if (parts < 32) parts = 32;
+    if (parts > most) parts = most;
+    a.parts = (int32_t)(parts > 1 ? parts : 1);
+    const int64_t j = (a.Nb * rows + 1023) / 1024;                // the join: as in mla_step.hip
+    a.join_rows = (int32_t)(j < rows ? j : rows);
+    return (size_t)a.groups * a.parts * 2 * (16 * a.waves) * (a.Dc + 4) * sizeof(float);
+}
+
+hipError_t launch_mla_step_mx(const MlaStepArgs& a, hipStream_t s) {
+    return a.bf16 ? launch_mx_dims<__bf16>(a, s) : launch_mx_dims<float>(a, s);
+}
+
+}  // namespace kda

@@ -104,6 +104,18 @@ __device__ __forceinline__ void load_lds16s(const char* g, int off, char* lds) {
                  : "s"(base), "v"(off), "s"(from)
                  : "memory");
 }
+// 4 bytes per lane, of the active lanes only, to `lds` + 4 * lane
+__device__ __forceinline__ void load_lds4s(const char* g, int off, char* lds) {
+    const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(KDA_LDS char*)lds);
+    const uint64_t u = reinterpret_cast<uint64_t>(g);
+    const uint64_t from = (uint64_t)__builtin_amdgcn_readfirstlane((uint32_t)(u >> 32)) << 32 |
+                          (uint32_t)__builtin_amdgcn_readfirstlane((uint32_t)u);
+    uint64_t t;
+    asm volatile("s_mov_b32 m0, %1\n\ts_mov_b64 %0, %3\n\tglobal_load_lds_dword %2, %0"
+                 : "=&s"(t)
+                 : "s"(base), "v"(off), "s"(from)
+                 : "memory");
+}
 // the same where `on` (uniform): no branch, which would end the compiler's
 // scheduling region. All lanes of the wave are active here.
 __device__ __forceinline__ void load_lds16s_if(bool on, const char* g, int off, char* lds) {

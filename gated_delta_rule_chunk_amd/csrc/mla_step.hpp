@@ -143,13 +143,13 @@ constexpr int kMaxParts = 256;  // mla_step_plan makes no more
 
 // A wave's part of a row of queries over parts p0 + at, + step, ...: the sums of
 // all columns, not yet divided by l.
-template <int DC>
+template <int DC, int MOST>
 __device__ __forceinline__ void join_row(const MlaStepArgs& a, int row, int p0, int p1, int at, int step, int lane,
                                          f32x4 (&s)[DC / 256], float& m, float& l) {
     const int group = row / (16 * a.waves), r = row % (16 * a.waves);
-    float pm[kMaxParts / 64], pl[kMaxParts / 64];        // all under way together
+    float pm[MOST / 64], pl[MOST / 64];        // all under way together
 #pragma unroll
-    for (int k = 0; k < kMaxParts / 64; ++k) {
+    for (int k = 0; k < MOST / 64; ++k) {
         const int p = p0 + 64 * k + lane;
         pm[k] = -INFINITY;
         pl[k] = 0.f;
@@ -161,13 +161,13 @@ __device__ __forceinline__ void join_row(const MlaStepArgs& a, int row, int p0, 
     }
     m = pm[0];
 #pragma unroll
-    for (int k = 1; k < kMaxParts / 64; ++k) m = fmaxf(m, pm[k]);
+    for (int k = 1; k < MOST / 64; ++k) m = fmaxf(m, pm[k]);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) m = fmaxf(m, __shfl_xor(m, d));
     const float ms = m == -INFINITY ? 0.f : m;
     l = 0.f;
 #pragma unroll
-    for (int k = 0; k < kMaxParts / 64; ++k) l += pl[k] * __builtin_amdgcn_exp2f(pm[k] - ms);
+    for (int k = 0; k < MOST / 64; ++k) l += pl[k] * __builtin_amdgcn_exp2f(pm[k] - ms);
 #pragma unroll
     for (int d = 1; d < 64; d <<= 1) l += __shfl_xor(l, d);
 #pragma unroll
@@ -184,7 +184,8 @@ __device__ __forceinline__ void join_row(const MlaStepArgs& a, int row, int p0, 
         }
     }
 }
-template <class T, int DC> __global__ __launch_bounds__(256) void mla_step_join_kernel(MlaStepArgs a, int blocks) {
+template <class T, int DC, int MOST = kMaxParts>
+__global__ __launch_bounds__(256) void mla_step_join_kernel(MlaStepArgs a, int blocks) {
     __shared__ __attribute__((aligned(16))) float sums[4][DC];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int M = a.Tq * a.H, b = blockIdx.x / blocks, row0 = blockIdx.x % blocks * a.join_rows;
@@ -216,7 +217,7 @@ template <class T, int DC> __global__ __launch_bounds__(256) void mla_step_join_
     };
     if (p1 - p0 < kFewParts) {
         for (int row = row0 + w; row < row1; row += 4) {
-            join_row<DC>(a, row, p0, p1, 0, 1, lane, s, m, l);
+            join_row<DC, MOST>(a, row, p0, p1, 0, 1, lane, s, m, l);
             const float inv = inverse();
 #pragma unroll
             for (int v = 0; v < DC / 256; ++v) store4(op + (int64_t)row * DC + 256 * v + 4 * lane, s[v], inv);
@@ -225,7 +226,7 @@ template <class T, int DC> __global__ __launch_bounds__(256) void mla_step_join_
         return;
     }
     for (int row = row0; row < row1; ++row) {
-        join_row<DC>(a, row, p0, p1, w, 4, lane, s, m, l);
+        join_row<DC, MOST>(a, row, p0, p1, w, 4, lane, s, m, l);
 #pragma unroll
         for (int v = 0; v < DC / 256; ++v) *reinterpret_cast<f32x4*>(&sums[w][256 * v + 4 * lane]) = s[v];
         __syncthreads();

@@ -11,8 +11,7 @@
  * scale is a byte e + 127. e is the smallest with max|c| <= 7 * 2^e, at most 125,
  * so that no rounding is off by more than 2^e; values are rounded to the nearest
  * multiple, ties to the even code, past 6 to 6. A block whose largest magnitude
- * is below 2^-100 is held as zeros (scale byte 0, which always stands for
- * zeros); a block with a NaN or an infinity as NaN (scale byte 255). The key
+ * is below 2^-100 is held as zeros (codes and scale byte 0); a block with a NaN or an infinity as NaN (scale byte 255). The key
  * part r that the heads share keeps its dtype: its scores are the sensitive
  * ones, and it is a ninth of a row's channels.
  * A page of page_size rows is, in this order,
@@ -68,7 +67,11 @@ kda_status kda_mla_cache_read_mx(const void* cache, const int32_t* page_table, c
 
 /*
  * kda_mla_step over the 4-bit cache. Arguments, rules and errors as there.
- * A NaN block reaches the sequences that hold it and no others.
+ * The scores of KDA_BF16 run on the scaled matrix instructions with the 4-bit
+ * codes as they stand; a query of bf16 is two 8-bit floats (e4m3) there, whose
+ * sum is the query itself except for channels below 2^-14 of the largest of
+ * their 32, which are off by at most 2^-21 of that. KDA_F32 runs on the float32
+ * matrix cores. A NaN block reaches the sequences that hold it and no others.
  */
 size_t kda_mla_step_mx_workspace_bytes(int32_t Nb, int32_t Tq, int32_t H, int32_t Dc, int32_t page_size,
                                        int32_t max_pages, kda_dtype dtype);

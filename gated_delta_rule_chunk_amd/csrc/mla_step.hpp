@@ -184,7 +184,7 @@ __device__ __forceinline__ void join_row(const MlaStepArgs& a, int row, int p0, 
         }
     }
 }
-template <class T, int DC, int MOST = kMaxParts>
+template <class T, int DC, int MOST = kMaxParts, int TILE = kTile>
 __global__ __launch_bounds__(256) void mla_step_join_kernel(MlaStepArgs a, int blocks) {
     __shared__ __attribute__((aligned(16))) float sums[4][DC];
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -192,7 +192,7 @@ __global__ __launch_bounds__(256) void mla_step_join_kernel(MlaStepArgs a, int b
     const int row1 = row0 + a.join_rows < M ? row0 + a.join_rows : M;
     int first = 0, total = 0, tiles = 0;
     for (int b0 = 0; b0 < a.Nb; b0 += 64) {
-        const Scan sq = scan_tiles(a, b0, lane);
+        const Scan sq = scan_tiles<TILE>(a, b0, lane);
         if (b >= b0 && b < b0 + 64) {
             tiles = __builtin_amdgcn_readlane(sq.cnt, b - b0);
             first = total + __builtin_amdgcn_readlane(sq.sum, b - b0) - tiles;

@@ -120,22 +120,18 @@ __global__ __launch_bounds__(512, 2) void mla_mx_step_bf16_kernel(MlaStepArgs a)
         // the first entries and the queries are under way together
         const int p0 = t0 * kRows >> ps, e = entry(p0);
         // step s multiplies the blocks s, s + NM, s + 2 NM and s + 3 NM
-        MxQuery16 qm[NM];
-        uint32_t qs = 0;                                          // their scale bytes
+        bf16x8 q[NM][4];
 #pragma unroll
         for (int s = 0; s < NM; ++s) {
-            bf16x8 x[4];
             const int g = lane >> 4;
 #pragma unroll
             for (int i = 0; i < 4; ++i)
-                x[i] = load8(qlp + 32 * (NM * ((g >> 1) + 2 * (i >> 1)) + s) + 16 * (g & 1) + 8 * (i & 1));
-            qm[s].set(x, lane);
-            qs |= qm[s].s << 8 * s;
-            __builtin_amdgcn_sched_barrier(0);                    // one after the other: their sources take registers, too
+                q[s][i] = load8(qlp + 32 * (NM * ((g >> 1) + 2 * (i >> 1)) + s) + 16 * (g & 1) + 8 * (i & 1));
         }
         bf16x8 qf[NS ? NS : 1];
 #pragma unroll
         for (int s = 0; s < NS; ++s) qf[s] = load8(qrp + 32 * s + 8 * (lane >> 4));
+        __builtin_amdgcn_sched_barrier(0);                        // all are under way
         keep(p0, e);
 
         // Sends tile t on its way to LDS; returns which of its quarters exist. Rows
@@ -183,6 +179,16 @@ __global__ __launch_bounds__(512, 2) void mla_mx_step_bf16_kernel(MlaStepArgs a)
                     ln / (NB / 4) < left ? *reinterpret_cast<const uint32_t*>(from_scales + 4 * ln) : 0u;
             return have;
         };
+        // Tile t lies in raw[(t - t0) % 2].
+        int h1 = fetch(t0, raw[0]);
+        MxQuery16 qm[NM];
+        uint32_t qs = 0;                                          // their scale bytes
+#pragma unroll
+        for (int s = 0; s < NM; ++s) {
+            qm[s].set(q[s], lane);
+            qs |= qm[s].s << 8 * s;
+            __builtin_amdgcn_sched_barrier(0);
+        }
         // A tile's latents as bf16: for 32 rows each blocks of 16 columns, 32 rows of
         // 32 bytes, which the transposing reads take in the order of the lanes. A
         // thread takes a block of 32 channels of a row; of 16 lanes (a row each) eight
@@ -362,8 +368,6 @@ __global__ __launch_bounds__(512, 2) void mla_mx_step_bf16_kernel(MlaStepArgs a)
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
-        // Tile t lies in raw[(t - t0) % 2].
-        int h1 = fetch(t0, raw[0]);
         wait_loads_and_lds();
         wg_barrier();
         int h2 = t0 + 1 < t1 ? fetch(t0 + 1, raw[1]) : 0;

@@ -153,7 +153,9 @@ def load_library(path: str = LIB_PATH):
     lib.kda_mla_step_mx.argtypes = lib.kda_mla_step.argtypes
     lib.kda_mla_step_mx.restype = ctypes.c_int
     lib.kda_mla_weigh.argtypes = ([P, I64, I64, I64, P, I64, I64, I64, P, P, P, P, P, I32, F] + [I32] * 8 +
-                                  [F, D, I32, P, P])
+                                  [F, D, I32, P, Z, P, P])
+    lib.kda_mla_weigh_workspace_bytes.argtypes = [I32] * 5 + [D, I32]
+    lib.kda_mla_weigh_workspace_bytes.restype = Z
     lib.kda_mla_weigh.restype = ctypes.c_int
     lib.kda_mla_evict_workspace_bytes.argtypes = [I32] * 3
     lib.kda_mla_evict_workspace_bytes.restype = Z
@@ -1197,7 +1199,13 @@ def _rows_i32(n):
     return min(int(n), 0x7fffffff)
 
 
-def mla_weigh(q_latent, q_rope, cache, page_table, seq_lens, lse, scale, weights, fresh=None, decay=1.0, out=None):
+def mla_weigh_workspace_bytes(Nb, Tq, H, Dc, Dr, dtype, form):
+    """Bytes of workspace kda_mla_weigh needs (form 1: 4-bit cache)."""
+    return int(load_library().kda_mla_weigh_workspace_bytes(Nb, Tq, H, Dc, Dr, _DTYPES[dtype], form))
+
+
+def mla_weigh(q_latent, q_rope, cache, page_table, seq_lens, lse, scale, weights, fresh=None, decay=1.0, out=None,
+              workspace=None):
     """Add to the cached rows' weights the attention that new tokens pay them
     (kda_mla_weigh): weights[n][j] = decay * weights[n][j] + the sum over the
     tokens and heads of their softmax's weight of row j.
@@ -1219,11 +1227,17 @@ def mla_weigh(q_latent, q_rope, cache, page_table, seq_lens, lse, scale, weights
         out = weights
     else:
         _need(out, "out", weights.shape, torch.float32, dev)
+    if workspace is None:
+        need = mla_weigh_workspace_bytes(Nb, Tq, H, Dc, Dr, dt, int(mx))
+        workspace = _workspace(None, need, dev) if need else None
+    else:
+        workspace = _workspace(workspace, 0, dev)
     with _on(dev):
         _check(lib.kda_mla_weigh(_ptr(q_latent), *_steps(q_latent, 0, 1, 2), _ptr(q_rope), *_steps(q_rope, 0, 1, 2),
                                  _ptr(cache), _ptr(page_table), _ptr(seq_lens), _ptr(lse), _ptr(weights),
                                  Tq if fresh is None else _rows_i32(fresh), float(decay), n_pages, page_size, max_pages, Nb,
-                                 Tq, H, Dc, Dr, float(scale), _DTYPES[dt], int(mx), _ptr(out), _stream(dev)))
+                                 Tq, H, Dc, Dr, float(scale), _DTYPES[dt], int(mx), _ptr(workspace),
+                                 0 if workspace is None else workspace.numel(), _ptr(out), _stream(dev)))
     return out
 
 

@@ -314,6 +314,7 @@ struct MlaWeighArgs {           // kda_mla_weigh
     int32_t fresh;
     float decay;
     bool mx;
+    char* split;                // workspace: queries in 8 bits (more than 128 rows of them, bf16, 4-bit cache)
 };
 struct MlaEvictArgs {           // kda_mla_evict
     char* cache;
@@ -339,6 +340,7 @@ hipError_t launch_mla_step_mx(const MlaStepArgs& a, hipStream_t stream);       /
 size_t mla_step_mx_plan(MlaStepArgs& a);
 hipError_t launch_mla_append_mx(const MlaAppendArgs& a, hipStream_t stream);
 hipError_t launch_mla_read_mx(const MlaReadArgs& a, hipStream_t stream);
+size_t mla_weigh_workspace(const MlaWeighArgs& a);
 hipError_t launch_mla_weigh(const MlaWeighArgs& a, hipStream_t stream);
 int64_t mla_evict_moves(int32_t page_shift, int32_t max_pages);                // of a sequence, at most
 hipError_t launch_mla_evict(const MlaEvictArgs& a, hipStream_t stream);

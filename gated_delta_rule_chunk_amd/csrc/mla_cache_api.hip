@@ -99,12 +99,20 @@ kda_status kda_mla_step_mx(const void* q_latent, int64_t q_latent_n, int64_t q_l
     return finish(fn, kda::launch_mla_step_mx(a, static_cast<hipStream_t>(stream)));
 }
 
+size_t kda_mla_weigh_workspace_bytes(int32_t Nb, int32_t Tq, int32_t H, int32_t Dc, int32_t Dr, kda_dtype dtype,
+                                     int32_t form) {
+    if (!step_sizes_ok(Nb, Tq, H) || (Dc != 256 && Dc != 512) || (Dr != 0 && Dr != 64)) return 0;
+    kda::MlaWeighArgs x{};
+    x.s.Nb = Nb; x.s.Tq = Tq; x.s.H = H; x.s.Dc = Dc; x.s.Dr = Dr; x.s.bf16 = dtype == KDA_BF16; x.mx = form == 1;
+    return kda::mla_weigh_workspace(x);
+}
+
 kda_status kda_mla_weigh(const void* q_latent, int64_t q_latent_n, int64_t q_latent_t, int64_t q_latent_h,
                          const void* q_rope, int64_t q_rope_n, int64_t q_rope_t, int64_t q_rope_h, const void* cache,
                          const int32_t* page_table, const int32_t* seq_lens, const float* lse, const float* weights,
                          int32_t fresh, float decay, int32_t n_pages, int32_t page_size, int32_t max_pages, int32_t Nb,
                          int32_t Tq, int32_t H, int32_t Dc, int32_t Dr, float scale, kda_dtype dtype, int32_t form,
-                         float* weights_out, void* stream) {
+                         void* workspace, size_t workspace_bytes, float* weights_out, void* stream) {
     const char* fn = "kda_mla_weigh";
     kda::clear_error();
     if (!step_sizes_ok(Nb, Tq, H)) return fail(KDA_ERR_INVALID_ARG, kStepSizes, fn, Nb, Tq, H);
@@ -126,6 +134,17 @@ kda_status kda_mla_weigh(const void* q_latent, int64_t q_latent_n, int64_t q_lat
     r.apart("weights_out", weights_out, "cache", cache);
     r.apart("weights_out", weights_out, "lse", lse);
     if (r.st != KDA_OK) return r.st;
+    const size_t need = kda_mla_weigh_workspace_bytes(Nb, Tq, H, Dc, Dr, dtype, form);
+    if (need && (!workspace || workspace_bytes < need || !aligned(workspace)))
+        return fail(KDA_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed, 16-byte aligned", fn,
+                    workspace ? workspace_bytes : 0, need);
+    if (need) {
+        r.apart("workspace", workspace, "cache", cache);
+        r.apart("workspace", workspace, "weights_out", weights_out);
+        r.apart("workspace", workspace, "q_latent", q_latent);
+        if (r.st != KDA_OK) return r.st;
+    }
+    x.split = static_cast<char*>(workspace);
     x.lse = lse; x.w_in = weights; x.w_out = weights_out; x.fresh = fresh; x.decay = decay; x.mx = form == 1;
     if (kda_status st = set_status(fn, x.s.status)) return st;
     return finish(fn, kda::launch_mla_weigh(x, static_cast<hipStream_t>(stream)));

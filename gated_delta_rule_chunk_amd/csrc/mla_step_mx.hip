@@ -11,7 +11,7 @@
 // all 32 rows with a quarter of the columns. So neither queries, scores nor outputs
 // (Dc / 8 registers) take more than a third of a SIMD's registers, and three
 // blocks (96 rows) leave each SIMD three waves.
-#include "mla_mx.hpp"
+#include "mla_mx_tile.hpp"
 #include "mla_step.hpp"
 
 namespace kda {
@@ -19,29 +19,6 @@ namespace {
 
 // float32: blocks of 32 rows of queries a workgroup, at most (as queries and outputs fit the registers)
 __host__ __device__ constexpr int most_blocks(int dc) { return dc == 256 ? 2 : 1; }
-// bf16: cache rows a tile, waves
-constexpr int kRows = 64, kWaves = 8;
-
-// Where the parts of a tile as it lies in memory come to in LDS: codes, shared
-// parts, scale bytes, each in four quarters of 16 rows. A row of codes is 16 or 8
-// chunks of 16 bytes, one of the shared part 8; chunk c lies at c ^ swz(r).
-// The scores' operand reads take, of 16 lanes that LDS serves at a time, 8 rows of
-// chunk c and 8 other rows of chunk c ^ 4, c ^ 2 (codes) or c ^ 1 (shared part):
-// rows 0-3 and 12-15, and 4-11. Under these permutations each takes every bank once.
-template <int DC, int DR> struct RawTile {
-    static constexpr int NB = DC / 32;
-    static constexpr int kCodes = 16 * DC / 2, kRope = 16 * DR * 2;                // bytes of 16 rows
-    static constexpr int kRopeAt = 4 * kCodes, kScalesAt = kRopeAt + 4 * kRope, kBytes = kScalesAt + 4 * 256;
-    static __device__ __forceinline__ int swz_codes(int r) {
-        if constexpr (NB == 16) return (r & 7) << 1 | ((r >> 3 ^ r >> 2) & 1);
-        else return (r >> 1 & 3) << 1 | ((r >> 3 ^ r >> 2) & 1);
-    }
-    static __device__ __forceinline__ int swz_rope(int r) { return r >> 1 & 7; }
-    static __device__ __forceinline__ int codes(int r, int c) { return r * (DC / 2) + ((c ^ swz_codes(r & 15)) << 4); }
-    static __device__ __forceinline__ int rope(int r, int c) { return kRopeAt + r * (DR * 2) + ((c ^ swz_rope(r & 15)) << 4); }
-    static __device__ __forceinline__ int scales(int r) { return kScalesAt + (r >> 4) * 256 + (r & 15) * NB; }
-};
-
 // bf16. Eight waves share up to six sets of 16 rows of queries and tiles of 64 keys.
 // For the scores a set has one wave, or two or four that take 16-key groups of the
 // tile each (and tell each other their maxima); every wave multiplies all rows'
@@ -134,50 +111,10 @@ __global__ __launch_bounds__(512, 2) void mla_mx_step_bf16_kernel(MlaStepArgs a)
         __builtin_amdgcn_sched_barrier(0);                        // all are under way
         keep(p0, e);
 
-        // Sends tile t on its way to LDS; returns which of its quarters exist. Rows
-        // past the length and of missing pages are zeros there: their weights are 0,
-        // but what these multiply has to be finite. Two waves load a quarter: of its
-        // instructions of 1 KB every other one, the first its scale bytes too.
-        const int quarter = w & 3, j0 = w >> 2;
         auto fetch = [&](int t, char* to) {
             const int k0 = t * kRows, p = k0 >> ps;
             if (p >= pbase + 64) keep(p, entry(p));
-            int have = 0;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) have |= (int)(exist >> (((k0 + 16 * q) >> ps) - pbase) & 1) << q;
-            const int kq = k0 + 16 * quarter, row = kq & ((1 << ps) - 1);
-            // (a missing page's address is not used)
-            const char* const page = static_cast<const char*>(a.cache) +
-                                     __builtin_amdgcn_readlane(pages, (kq >> ps) - pbase) * page_bytes;
-            const char* const from_codes = page + (int64_t)row * (DC / 2);
-            const char* const from_scales = page + (((int64_t)DC / 2) << ps) + row * NB;
-            const char* const from_rope = page + (((int64_t)DC / 2 + NB) << ps) + (int64_t)row * (DR * 2);
-            int ln = lane;
-            asm volatile("" : "+v"(ln));                          // offsets are formed here, not kept in registers
-            const int rc = (1024 / (DC / 2)) * j0 + ln / NB, off = rc * (DC / 2) + (((ln % NB) ^ Raw::swz_codes(rc)) << 4);
-            const int rr = 8 * j0 + ln / 8, off_rope = rr * 128 + (((ln % 8) ^ Raw::swz_rope(rr)) << 4);
-            char* const to_codes = to + quarter * Raw::kCodes + j0 * 1024;
-            char* const to_rope = to + Raw::kRopeAt + quarter * Raw::kRope + j0 * 1024;
-            char* const to_scales = to + Raw::kScalesAt + quarter * 256;
-            if (have == 15 && k0 + kRows <= rows) {
-                load_lds16s(from_codes, off, to_codes);
-                // 8 rows on: the permutations differ in one bit
-                if constexpr (NB == 16) load_lds16s(from_codes, (off ^ 16) + 2048, to_codes + 2048);
-                if constexpr (DR > 0) load_lds16s(from_rope, off_rope, to_rope);
-                if (j0 == 0 && (NB == 16 || ln < 32)) load_lds4s(from_scales, 4 * ln, to_scales);
-                return have;
-            }
-            const int left = have >> quarter & 1 ? rows - kq : 0; // rows of the quarter to be read
-            auto copy = [&](char* at, const char* from, bool there) {
-                *reinterpret_cast<u32x4*>(at + 16 * ln) = there ? *reinterpret_cast<const u32x4*>(from) : u32x4{0, 0, 0, 0};
-            };
-            copy(to_codes, from_codes + off, rc < left);
-            if constexpr (NB == 16) copy(to_codes + 2048, from_codes + (off ^ 16) + 2048, rc + 8 < left);
-            if constexpr (DR > 0) copy(to_rope, from_rope + off_rope, rr < left);
-            if (j0 == 0 && (NB == 16 || ln < 32))
-                *reinterpret_cast<uint32_t*>(to_scales + 4 * ln) =
-                    ln / (NB / 4) < left ? *reinterpret_cast<const uint32_t*>(from_scales + 4 * ln) : 0u;
-            return have;
+            return mx_fetch<DC, DR>(to, static_cast<const char*>(a.cache), page_bytes, pages, exist, pbase, ps, k0, rows, w, lane);
         };
         // Tile t lies in raw[(t - t0) % 2].
         int h1 = fetch(t0, raw[0]);
@@ -225,59 +162,9 @@ __global__ __launch_bounds__(512, 2) void mla_mx_step_bf16_kernel(MlaStepArgs a)
 #pragma unroll
             for (int d = 0; d < ND; ++d) acc[s][d] = f32x4{0.f, 0.f, 0.f, 0.f};
         float m = -INFINITY, lsum = 0.f;
-        // The products of the scores of the wave's keys in a tile, in chains of 16
-        // keys, each step's operands read under the one before.
         f32x4 sc[NG];
         float mx = -INFINITY;
-        auto products = [&](const char* buf) {
-            int ln = lane;
-            asm volatile("" : "+v"(ln));                          // LDS addresses are formed here, not kept over the loop
-            const int g = ln >> 4, n = ln & 15, r0 = 16 * NG * kg + n;
-            uint32_t ks[NG];
-            u32x4 x[2][NG];
-            auto read = [&](int i) {
-#pragma unroll
-                for (int h = 0; h < NG; ++h) x[i & 1][h] = *reinterpret_cast<const u32x4*>(buf + Raw::codes(r0 + 16 * h, NM * g + i));
-            };
-#pragma unroll
-            for (int h = 0; h < NG; ++h) {
-                sc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
-                if constexpr (NM == 4) ks[h] = *reinterpret_cast<const uint32_t*>(buf + Raw::scales(r0 + 16 * h) + 4 * g);
-                else ks[h] = *reinterpret_cast<const uint16_t*>(buf + Raw::scales(r0 + 16 * h) + 2 * g);
-            }
-            read(0);
-            bf16x8 y[NG];
-            auto rope = [&](int s) {
-#pragma unroll
-                for (int h = 0; h < NG; ++h) y[h] = *reinterpret_cast<const bf16x8*>(buf + Raw::rope(r0 + 16 * h, 4 * s + g));
-            };
-            auto step = [&](auto I) {
-                constexpr int i = I.value;
-                if constexpr (i + 1 < NM) read(i + 1);
-                else if constexpr (NS > 0) rope(0);
-#pragma unroll
-                for (int h = 0; h < NG; ++h) sc[h] = mma_mx16<i>(x[i & 1][h], qm[i].hi, sc[h], ks[h], qs);
-#pragma unroll
-                for (int h = 0; h < NG; ++h)
-                    sc[h] = mma_mx16<i>(x[i & 1][h], qm[i].lo, sc[h], ks[h], qs - 0x04040404u);         // (no byte is below 4; NaN's stays large)
-                __builtin_amdgcn_sched_barrier(0);
-            };
-            step(std::integral_constant<int, 0>{});
-            step(std::integral_constant<int, 1>{});
-            if constexpr (NM == 4) {
-                step(std::integral_constant<int, 2>{});
-                step(std::integral_constant<int, 3>{});
-            }
-#pragma unroll
-            for (int s = 0; s < NS; ++s) {
-#pragma unroll
-                for (int h = 0; h < NG; ++h) sc[h] = mma16(y[h], qf[s], sc[h]);
-                if (s + 1 < NS) rope(s + 1);
-            }
-            // (sends the products on their way here: the compiler would move them behind what follows)
-#pragma unroll
-            for (int h = 0; h < NG; ++h) asm volatile("" : "+v"(sc[h]));
-        };
+        auto products = [&](const char* buf) { mx_scores<DC, DR, NG>(buf, 16 * NG * kg, lane, qm, qs, qf, sc); };
         // hides what the rows of tile t do not see; their maxima over the wave's keys
         auto maxima = [&](int t, int have) {
             int ln = lane;

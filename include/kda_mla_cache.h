@@ -99,17 +99,23 @@ kda_status kda_mla_step_mx(const void* q_latent, int64_t q_latent_n, int64_t q_l
  *              rows, or more, after a prefill.) >= 0
  *   decay      in [0, 1]; 1 sums all steps, less forgets, 0 starts anew (and reads
  *              no weight)
+ *   workspace  at least kda_mla_weigh_workspace_bytes(...) bytes, 16-byte aligned;
+ *              calls that may run at the same time need their own. NULL where that
+ *              is 0: it is not for KDA_BF16 over the 4-bit cache with Tq * H > 128
+ *              (18 KB for 16 of these rows, Dc = 512, Dr = 64)
  * Sums are float32, in an order that the sizes decide: the same inputs give the
  * same bits. Rows in missing pages get no new weight and are reported as in
  * kda_mla_step. Limits as in kda_mla_step. Nb * Tq = 0 is a no-op: nothing is
  * written.
  */
+size_t kda_mla_weigh_workspace_bytes(int32_t Nb, int32_t Tq, int32_t H, int32_t Dc, int32_t Dr, kda_dtype dtype,
+                                     int32_t form);
 kda_status kda_mla_weigh(const void* q_latent, int64_t q_latent_n, int64_t q_latent_t, int64_t q_latent_h,
                          const void* q_rope, int64_t q_rope_n, int64_t q_rope_t, int64_t q_rope_h, const void* cache,
                          const int32_t* page_table, const int32_t* seq_lens, const float* lse, const float* weights,
                          int32_t fresh, float decay, int32_t n_pages, int32_t page_size, int32_t max_pages, int32_t Nb,
                          int32_t Tq, int32_t H, int32_t Dc, int32_t Dr, float scale, kda_dtype dtype, int32_t form,
-                         float* weights_out, void* stream);
+                         void* workspace, size_t workspace_bytes, float* weights_out, void* stream);
 
 /*
  * Evicts rows by whole pages. With ps = page_size, of a sequence of L rows

@@ -29,7 +29,7 @@ def lib():
 def test_header_symbols_are_exported(lib):
     names = set(kda.declared_symbols(HEADER))
     assert names == {"kda_mla_mx_row_bytes", "kda_mla_cache_append_mx", "kda_mla_cache_read_mx", "kda_mla_step_mx",
-                     "kda_mla_step_mx_workspace_bytes", "kda_mla_weigh", "kda_mla_evict",
+                     "kda_mla_step_mx_workspace_bytes", "kda_mla_weigh", "kda_mla_weigh_workspace_bytes", "kda_mla_evict",
                      "kda_mla_evict_workspace_bytes"}
     out = subprocess.run(["nm", "-D", "--defined-only", kda.LIB_PATH], capture_output=True, text=True, check=True).stdout
     assert names <= {line.split()[-1] for line in out.splitlines() if " T " in line}
@@ -83,11 +83,11 @@ def _step(lib, ws=P[5], n=1 << 30, o=P[6], lse=P[7], **kw):
                                a["Dc"], a["Dr"], a["scale"], a["dtype"], ws, n, o, lse, None)
 
 
-def _weigh(lib, lse=P[5], w=P[6], fresh=1, decay=1.0, form=1, out=P[7], **kw):
+def _weigh(lib, lse=P[5], w=P[6], fresh=1, decay=1.0, form=1, out=P[7], ws=None, n=0, **kw):
     a = {**STEP, **kw}
     return lib.kda_mla_weigh(a["ql"], a["ln"], a["lt"], a["lh"], a["qr"], a["rn"], a["rt"], a["rh"], a["cache"],
                              a["table"], a["lens"], lse, w, fresh, decay, a["n_pages"], a["page"], a["max_pages"],
-                             a["B"], a["T"], a["H"], a["Dc"], a["Dr"], a["scale"], a["dtype"], form, out, None)
+                             a["B"], a["T"], a["H"], a["Dc"], a["Dr"], a["scale"], a["dtype"], form, ws, n, out, None)
 
 
 def _evict(lib, **kw):
@@ -151,6 +151,8 @@ def test_step_refuses(lib, kw, status, needle):
     (dict(fresh=-1), BAD, "fresh"), (dict(decay=-0.1), BAD, "decay"), (dict(decay=1.5), BAD, "decay"),
     (dict(decay=float("nan")), BAD, "decay"), (dict(form=2), BAD, "form"), (dict(out=P[2]), BAD, "alias cache"),
     (dict(out=P[5]), BAD, "alias lse"), (dict(out=P[0]), BAD, "alias q_latent"),
+    (dict(H=129), BAD, "workspace"), (dict(H=129, ws=P[8], n=1000), BAD, "workspace"), (dict(H=129, ws=ODD, n=1 << 30), BAD, "workspace"),
+    (dict(H=129, ws=P[7], n=1 << 30), BAD, "workspace must not alias weights_out"),
 ])
 def test_weigh_refuses(lib, kw, status, needle):
     assert _weigh(lib, **kw) == status
@@ -176,6 +178,10 @@ def test_workspace_bytes(lib):
     assert w(4, 1, 96, 512, 64, 128, torch.bfloat16) > 0
     assert w(4, 1, 96, 512, 48, 128, torch.bfloat16) == w(4, 1, 96, 128, 64, 128, torch.bfloat16) == 0
     assert w(0, 1, 96, 512, 64, 128, torch.bfloat16) == w(4, 1, 96, 512, 64, 0, torch.bfloat16) == 0
+    g = kda.mla_weigh_workspace_bytes
+    assert g(4, 1, 128, 512, 64, torch.bfloat16, 1) == g(4, 3, 96, 512, 64, torch.bfloat16, 0) == 0
+    assert g(4, 3, 96, 512, 64, torch.float32, 1) == g(4, 3, 96, 384, 64, torch.bfloat16, 1) == 0
+    assert g(4, 3, 96, 512, 64, torch.bfloat16, 1) >= 4 * 18 * 16 * 1088
     e = kda.mla_evict_workspace_bytes
     assert e(1, 16, 1) > 0 and e(100, 64, 128) >= 100 * (64 * 128 + 128) * 4
     assert e(0, 16, 1) == e(1, 24, 1) == e(1, 16, 0) == e(1, 1 << 20, 1 << 12) == 0

@@ -324,7 +324,7 @@ struct MlaEvictArgs {           // kda_mla_evict
     int32_t* table_out;
     int32_t* lens_out;
     float* w_out;
-    int32_t* moves;             // workspace: [Nb] numbers of moves, then [Nb][2][moves at most] destinations and sources
+    int32_t* work;              // workspace
     unsigned int* status;
     int32_t n_pages, page_shift, max_pages, Nb, keep, first, recent;
     // a row's pieces in a page: `units` of 16 bytes, of which those behind the first
@@ -342,7 +342,8 @@ hipError_t launch_mla_append_mx(const MlaAppendArgs& a, hipStream_t stream);
 hipError_t launch_mla_read_mx(const MlaReadArgs& a, hipStream_t stream);
 size_t mla_weigh_workspace(const MlaWeighArgs& a);
 hipError_t launch_mla_weigh(const MlaWeighArgs& a, hipStream_t stream);
-int64_t mla_evict_moves(int32_t page_shift, int32_t max_pages);                // of a sequence, at most
+size_t mla_evict_workspace(int32_t Nb, int32_t page_shift, int32_t max_pages);
+int64_t mla_evict_workgroups(int32_t Nb, int32_t page_shift, int32_t max_pages);      // of 1024 threads
 hipError_t launch_mla_evict(const MlaEvictArgs& a, hipStream_t stream);
 hipError_t launch_mla_fwd(const MlaArgs& a, hipStream_t stream);
 hipError_t launch_mla_bwd(const MlaArgs& a, hipStream_t stream);

@@ -11,11 +11,10 @@ kda_status check_form(const char* fn, int32_t form) {
     return KDA_OK;
 }
 
-size_t evict_workspace(int32_t Nb, int32_t page_size, int32_t max_pages) {
+int shift_of(int32_t page_size) {
     int shift = 0;
     while ((1 << shift) < page_size) ++shift;
-    return 4 * (((size_t)Nb + 3) / 4 * 4 + (size_t)Nb * 2 * (size_t)kda::mla_evict_moves(shift, max_pages) +
-                (size_t)Nb * max_pages);
+    return shift;
 }
 
 }  // namespace
@@ -151,10 +150,10 @@ kda_status kda_mla_weigh(const void* q_latent, int64_t q_latent_n, int64_t q_lat
 }
 
 size_t kda_mla_evict_workspace_bytes(int32_t Nb, int32_t page_size, int32_t max_pages) {
-    if (Nb < 1 || Nb > (1 << 22) || page_size < 16 || page_size > (1 << 24) || (page_size & (page_size - 1)) ||
+    if (Nb < 1 || Nb >= (1 << 22) || page_size < 16 || page_size > (1 << 24) || (page_size & (page_size - 1)) ||
         max_pages < 1 || (int64_t)max_pages * page_size > ((int64_t)1 << 30))
         return 0;
-    return evict_workspace(Nb, page_size, max_pages);
+    return kda::mla_evict_workspace(Nb, shift_of(page_size), max_pages);
 }
 
 kda_status kda_mla_evict(void* cache, const int32_t* page_table, const int32_t* seq_lens, const float* weights,
@@ -164,7 +163,7 @@ kda_status kda_mla_evict(void* cache, const int32_t* page_table, const int32_t* 
                          float* weights_out, void* stream) {
     const char* fn = "kda_mla_evict";
     kda::clear_error();
-    if (Nb < 0 || Nb > (1 << 22)) return fail(KDA_ERR_INVALID_ARG, "%s: need 0 <= Nb <= 2^22, got %d", fn, Nb);
+    if (Nb < 0 || Nb >= (1 << 22)) return fail(KDA_ERR_INVALID_ARG, "%s: need 0 <= Nb < 2^22, got %d", fn, Nb);
     if (Nb == 0) return KDA_OK;
     kda::MlaEvictArgs a{};
     if (kda_status st = check_cache(fn, cache, page_table, seq_lens, n_pages, page_size, max_pages, Dc, Dr, dtype,
@@ -176,7 +175,10 @@ kda_status kda_mla_evict(void* cache, const int32_t* page_table, const int32_t* 
                     recent);
     if (!weights || !page_table_out || !seq_lens_out || !weights_out)
         return fail(KDA_ERR_INVALID_ARG, "%s: weights and the three outputs must be non-NULL", fn);
-    const size_t need = evict_workspace(Nb, page_size, max_pages);
+    if (kda::mla_evict_workgroups(Nb, a.page_shift, max_pages) >= (1 << 22))
+        return fail(KDA_ERR_UNSUPPORTED, "%s: problem too large: Nb = %d sequences of up to %lld rows", fn, Nb,
+                    (long long)max_pages * page_size);
+    const size_t need = kda::mla_evict_workspace(Nb, a.page_shift, max_pages);
     if (!workspace || workspace_bytes < need || !aligned(workspace))
         return fail(KDA_ERR_INVALID_ARG, "%s: workspace of %zu bytes, %zu needed, 16-byte aligned", fn,
                     workspace ? workspace_bytes : 0, need);
@@ -195,7 +197,7 @@ kda_status kda_mla_evict(void* cache, const int32_t* page_table, const int32_t* 
     const int es = dtype == KDA_BF16 ? 2 : 4;
     a.cache = static_cast<char*>(cache); a.table = page_table; a.lens = seq_lens; a.w_in = weights;
     a.table_out = page_table_out; a.lens_out = seq_lens_out; a.w_out = weights_out;
-    a.moves = static_cast<int32_t*>(workspace);
+    a.work = static_cast<int32_t*>(workspace);
     a.n_pages = n_pages; a.max_pages = max_pages; a.Nb = Nb; a.keep = keep; a.first = first; a.recent = recent;
     a.codes = form ? Dc / 32 : (Dc + Dr) * es / 16;
     a.scale_bytes = form ? Dc / 32 : 0;

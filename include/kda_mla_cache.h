@@ -145,7 +145,8 @@ kda_status kda_mla_weigh(const void* q_latent, int64_t q_latent_n, int64_t q_lat
  *               calls that may run at the same time need their own
  * A sequence longer than its page table, or with a page among a .. b-1 that does
  * not exist, stays as it is and is reported by kda_device_check. Nb = 0 is a
- * no-op. Nb at most 2^22.
+ * no-op. Nb below 2^22; with page tables of R > 16384 rows,
+ * Nb * min(ceil(R / 2048), 1024) too.
  */
 size_t kda_mla_evict_workspace_bytes(int32_t Nb, int32_t page_size, int32_t max_pages);
 kda_status kda_mla_evict(void* cache, const int32_t* page_table, const int32_t* seq_lens, const float* weights,

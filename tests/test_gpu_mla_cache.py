@@ -518,6 +518,38 @@ def test_evict_long_sequences_and_many():
         _evict_and_check(cache, table, _i32(lens), w, keep, 0, 64, True)
 
 
+@pytest.mark.parametrize("in_place", [False, True])
+@pytest.mark.parametrize("kind", ["equal", "two", "odd", "falling", "rising", "any"])
+@pytest.mark.parametrize("cap", [16384, 16400, 1 << 21, (1 << 21) + 4096])
+def test_evict_of_page_tables_of_any_room(cap, kind, in_place):
+    lens, page = [16384, 40001, 700, 0, 4097, -1], 16
+    lens[1] = min(lens[1], cap)
+    g = torch.Generator(device="cuda").manual_seed(75)
+    table, total = _table(lens, page, g, 1)
+    wide = torch.full((len(lens), cap // page), -7, dtype=torch.int32)
+    m = min(table.shape[1], wide.shape[1])
+    wide[:, :m] = table[:, :m]
+    cache = torch.randint(0, 255, (total, page, 136), dtype=torch.uint8, device="cuda", generator=g)
+    N = 40016
+    j = torch.arange(N, device="cuda").float().expand(len(lens), -1)
+    u = torch.randint(0, 6, (len(lens), N), generator=g, device="cuda")
+    odd = torch.tensor([math.nan, math.inf, -0.0, 0.0, -1.0, 1e-42], device="cuda")[u]
+    some = {"equal": torch.ones_like(j), "two": 1.0 + (u % 2), "odd": odd, "falling": 1e5 - j, "rising": 1 + j / 7,
+            "any": _weights(g, len(lens), N)}[kind]
+    w = torch.full((len(lens), cap), 3.0, device="cuda")
+    w[:, :min(N, cap)] = some[:, :cap]
+    _evict_and_check(cache, wide.cuda(), _i32(lens), w, 3000, 20, 40, in_place)
+
+
+def test_evict_keeps_the_order_of_many_recent_rows():
+    lens, page = [30000, 9000], 16
+    g = torch.Generator(device="cuda").manual_seed(76)
+    table, total = _table(lens, page, g, 1)
+    cache = torch.randint(0, 255, (total, page, 136), dtype=torch.uint8, device="cuda", generator=g)
+    w = _weights(g, 2, table.shape[1] * page)
+    _evict_and_check(cache, table.cuda(), _i32(lens), w, 1000, 100, 8500, True)
+
+
 def test_evict_refuses_sequences_with_missing_pages():
     lens, page = [200, 200, 90, 5000], 16
     cache, table, _ = _cache([200, 200, 90, 208], page, 512, 64, BF16, 73)

@@ -160,7 +160,8 @@ def test_weigh_refuses(lib, kw, status, needle):
 
 
 @pytest.mark.parametrize("kw,status,needle", CACHE + LENS + [
-    (dict(B=-1), BAD, "Nb"), (dict(B=(1 << 22) + 1), BAD, "Nb"), (dict(form=-1), BAD, "form"), (dict(keep=-1), BAD, "keep"),
+    (dict(B=-1), BAD, "Nb"), (dict(B=1 << 22), BAD, "Nb"), (dict(B=8192, max_pages=1 << 16, page=64), UNSUP, "too large"),
+    (dict(form=-1), BAD, "form"), (dict(keep=-1), BAD, "keep"),
     (dict(first=-1), BAD, "first"), (dict(recent=-1), BAD, "recent"), (dict(w=None), BAD, "weights"),
     (dict(tout=None), BAD, "outputs"), (dict(lout=None), BAD, "outputs"), (dict(wout=None), BAD, "outputs"),
     (dict(ws=None), BAD, "workspace"), (dict(n=100), BAD, "workspace"), (dict(ws=ODD), BAD, "workspace"),
@@ -183,7 +184,7 @@ def test_workspace_bytes(lib):
     assert g(4, 3, 96, 512, 64, torch.float32, 1) == g(4, 3, 96, 384, 64, torch.bfloat16, 1) == 0
     assert g(4, 3, 96, 512, 64, torch.bfloat16, 1) >= 4 * 18 * 16 * 1088
     e = kda.mla_evict_workspace_bytes
-    assert e(1, 16, 1) > 0 and e(100, 64, 128) >= 100 * (64 * 128 + 128) * 4
+    assert e(1, 16, 1) > 0 and e(100, 64, 128) >= 100 * 64 * 64 * 3 * 4
     assert e(0, 16, 1) == e(1, 24, 1) == e(1, 16, 0) == e(1, 1 << 20, 1 << 12) == 0
 
 

@@ -31,6 +31,13 @@ struct MxScale {
     }
 };
 
+// The two codes of byte I as bf16, with a scale each: the exponents of a and b.
+template <int I> __device__ __forceinline__ uint32_t mx_pair(uint32_t c, uint32_t a, uint32_t b) {
+    const uint32_t lo = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, __uint_as_float(a), I));
+    const uint32_t hi = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, __uint_as_float(b), I));
+    return (lo & 0xffffu) | (hi & 0xffff0000u);
+}
+
 typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
 // bf16 queries as the sum of two e4m3 numbers each, hi 2^(s - 127) + lo 2^(s - 131),

@@ -12,10 +12,12 @@ constexpr int kRows = 64, kWaves = 8;    // of a tile, of a workgroup
 
 // Where the parts of a tile as it lies in memory come to in LDS: codes, shared
 // parts, scale bytes, each in four quarters of 16 rows. A row of codes is 16 or 8
-// chunks of 16 bytes, one of the shared part 8; chunk c lies at c ^ swz(r).
+// chunks of 16 bytes, one of the shared part 8; chunk c lies at c ^ swz(r), that of codes
+// at c ^ swz(r) ^ swz_quarter(quarter).
 // The scores' operand reads take, of 16 lanes that LDS serves at a time, 8 rows of
 // chunk c and 8 other rows of chunk c ^ 4, c ^ 2 (codes) or c ^ 1 (shared part):
-// rows 0-3 and 12-15, and 4-11. Under these permutations each takes every bank once.
+// rows 0-3 and 12-15, and 4-11; the outputs' transposing reads 8 bytes of chunk c of
+// four rows in each quarter. Under these permutations each takes every bank once.
 template <int DC, int DR> struct RawTile {
     static constexpr int NB = DC / 32;
     static constexpr int kCodes = 16 * DC / 2, kRope = 16 * DR * 2;                // bytes of 16 rows
@@ -24,11 +26,24 @@ template <int DC, int DR> struct RawTile {
         if constexpr (NB == 16) return (r & 7) << 1 | ((r >> 3 ^ r >> 2) & 1);
         else return (r >> 1 & 3) << 1 | ((r >> 3 ^ r >> 2) & 1);
     }
+    static __device__ __forceinline__ int swz_quarter(int q) { return (q & 1) | (q >> 1) << (NB == 16 ? 3 : 2); }
     static __device__ __forceinline__ int swz_rope(int r) { return r >> 1 & 7; }
-    static __device__ __forceinline__ int codes(int r, int c) { return r * (DC / 2) + ((c ^ swz_codes(r & 15)) << 4); }
+    static __device__ __forceinline__ int codes(int r, int c) {
+        return r * (DC / 2) + ((c ^ swz_codes(r & 15) ^ swz_quarter(r >> 4)) << 4);
+    }
     static __device__ __forceinline__ int rope(int r, int c) { return kRopeAt + r * (DR * 2) + ((c ^ swz_rope(r & 15)) << 4); }
     static __device__ __forceinline__ int scales(int r) { return kScalesAt + (r >> 4) * 256 + (r & 15) * NB; }
 };
+
+// Waits for this wave's LDS accesses and its loads, but for those of the last whole
+// tile that it sent on its way (mx_fetch; loads come back in their order).
+template <int DC, int DR> __device__ __forceinline__ void wait_but_last_tile(int w) {
+    constexpr int kLoads = DC / 256 + (DR > 0);
+    asm volatile("" ::: "memory");
+    if (w < 4) __builtin_amdgcn_s_waitcnt(0x0070 | (kLoads + 1));
+    else __builtin_amdgcn_s_waitcnt(0x0070 | kLoads);
+    asm volatile("" ::: "memory");
+}
 
 // Sends the tile of rows k0 .. k0 + 63 of a sequence (of `rows`) on its way to LDS
 // by eight waves (this one w); returns which of its quarters of 16 rows exist. Rows past the
@@ -54,7 +69,7 @@ __device__ __forceinline__ int mx_fetch(char* to, const char* cache, int64_t pag
     const char* const from_rope = page + (((int64_t)DC / 2 + NB) << ps) + (int64_t)row * (DR * 2);
     int ln = lane;
     asm volatile("" : "+v"(ln));                          // offsets are formed here, not kept in registers
-    const int rc = (1024 / (DC / 2)) * j0 + ln / NB, off = rc * (DC / 2) + (((ln % NB) ^ Raw::swz_codes(rc)) << 4);
+    const int rc = (1024 / (DC / 2)) * j0 + ln / NB, off = rc * (DC / 2) + (((ln % NB) ^ Raw::swz_codes(rc) ^ Raw::swz_quarter(quarter)) << 4);
     const int rr = 8 * j0 + ln / 8, off_rope = rr * 128 + (((ln % 8) ^ Raw::swz_rope(rr)) << 4);
     char* const to_codes = to + quarter * Raw::kCodes + j0 * 1024;
     char* const to_rope = to + Raw::kRopeAt + quarter * Raw::kRope + j0 * 1024;

@@ -19,6 +19,8 @@ namespace {
 
 // float32: blocks of 32 rows of queries a workgroup, at most (as queries and outputs fit the registers)
 __host__ __device__ constexpr int most_blocks(int dc) { return dc == 256 ? 2 : 1; }
+// bf16: workgroups a compute unit, as registers and LDS allow
+__host__ __device__ constexpr int residents(int dc, int sets) { return sets == 1 || (sets == 2 && dc == 256) ? 2 : 1; }
 // bf16. Eight waves share up to six sets of 16 rows of queries and tiles of 64 keys.
 // For the scores a set has one wave, or two or four that take 16-key groups of the
 // tile each (and tell each other their maxima); every wave multiplies all rows'
@@ -27,16 +29,18 @@ __host__ __device__ constexpr int most_blocks(int dc) { return dc == 256 ? 2 : 1
 // before; the softmax and the widening of the latents to bf16 come between; the
 // loads of the next tile, straight into LDS, are under way all the while.
 template <int DC, int DR, int S>
-__global__ __launch_bounds__(512, 2) void mla_mx_step_bf16_kernel(MlaStepArgs a) {
+__global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_kernel(MlaStepArgs a) {
     using T = __bf16;
     using Raw = RawTile<DC, DR>;
     // waves of a set, 16-key groups of each
     constexpr int KS = S == 6 ? 1 : S == 4 ? 2 : 4, NG = 4 / KS;
     constexpr int ND = DC / 16 / kWaves, NB = DC / 32, NM = DC / 128, NS = DR / 32;
-    __shared__ __attribute__((aligned(1024))) char raw[2][Raw::kBytes];
-    __shared__ __attribute__((aligned(1024))) char wide[kRows * DC * 2];
-    __shared__ __attribute__((aligned(16))) bf16x4 probs[2][S][64][2];   // of 32 keys each: operands
-    __shared__ float factor[S][16], tops[S][KS][16];
+    constexpr int PB = KS == 1 ? 2 : 1;                          // one barrier a tile, or two
+    constexpr int BUFS = S <= 2 ? 3 : 4;
+    __shared__ __attribute__((aligned(1024))) char raw[BUFS][Raw::kBytes];
+    __shared__ __attribute__((aligned(16))) bf16x4 probs[PB][2][S][64][2];   // of 32 keys each: operands
+    __shared__ __attribute__((aligned(16))) uint8_t scales[2][NB][kRows];    // of a tile, by blocks
+    __shared__ float factor[PB][S][16], tops[S][KS][16];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool scorer = w < S * KS;
     const int set = scorer ? w / KS : 0, kg = w % KS;
@@ -116,8 +120,8 @@ __global__ __launch_bounds__(512, 2) void mla_mx_step_bf16_kernel(MlaStepArgs a)
             if (p >= pbase + 64) keep(p, entry(p));
             return mx_fetch<DC, DR>(to, static_cast<const char*>(a.cache), page_bytes, pages, exist, pbase, ps, k0, rows, w, lane);
         };
-        // Tile t lies in raw[(t - t0) % 2].
-        int h1 = fetch(t0, raw[0]);
+        // Tile t lies in raw[(t - t0) % BUFS].
+        int h0 = fetch(t0, raw[0]);
         MxQuery16 qm[NM];
         uint32_t qs = 0;                                          // their scale bytes
 #pragma unroll
@@ -126,34 +130,15 @@ __global__ __launch_bounds__(512, 2) void mla_mx_step_bf16_kernel(MlaStepArgs a)
             qs |= qm[s].s << 8 * s;
             __builtin_amdgcn_sched_barrier(0);
         }
-        // A tile's latents as bf16: for 32 rows each blocks of 16 columns, 32 rows of
-        // 32 bytes, which the transposing reads take in the order of the lanes. A
-        // thread takes a block of 32 channels of a row; of 16 lanes (a row each) eight
-        // write the second half of a row when the others write the first, so that they take all banks.
-        auto widen = [&](const char* from) {
+        // a tile's scale bytes, turned: outputs take four keys of a block together
+        auto turn = [&](const char* from, int b) {
             int ln = lane;
             asm volatile("" : "+v"(ln));
-            const int odd_half = ln >> 3 & 1;
-            auto block = [&](int blk) {
-                const u32x4 c = *reinterpret_cast<const u32x4*>(from + Raw::codes(ln, blk));
-                const MxScale f(*reinterpret_cast<const uint8_t*>(from + Raw::scales(ln) + blk));
-                char* const to = wide + (ln >> 5) * (32 * DC * 2) + blk * 2048 + (ln & 31) * 32;
-                char* const at = to + 16 * odd_half;
-                char* const other = to + 16 * (odd_half ^ 1);
-                *reinterpret_cast<bf16x8*>(at) = f.bf16(odd_half ? c[1] : c[0]);
-                *reinterpret_cast<bf16x8*>(other) = f.bf16(odd_half ? c[0] : c[1]);
-                *reinterpret_cast<bf16x8*>(at + 1024) = f.bf16(odd_half ? c[3] : c[2]);
-                *reinterpret_cast<bf16x8*>(other + 1024) = f.bf16(odd_half ? c[2] : c[3]);
-            };
-            if constexpr (S == 6 && NB == 16) {                   // two waves have no softmax: five blocks each, the others one
-                block(w);
-                if (!scorer) {
+            const int q = kWaves - 1 - w;                         // (the last waves have no scores, or the fewest)
+            if (q < NB / 4) {
+                const uint32_t x = *reinterpret_cast<const uint32_t*>(from + Raw::scales(ln) + 4 * q);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) block(8 + 4 * (w - 6) + i);
-                }
-            } else {
-#pragma unroll
-                for (int i = 0; i < NB / kWaves; ++i) block(i * kWaves + w);
+                for (int i = 0; i < 4; ++i) scales[b][4 * q + i][ln] = (uint8_t)(x >> 8 * i);
             }
         };
         f32x4 acc[S][ND];
@@ -190,7 +175,7 @@ __global__ __launch_bounds__(512, 2) void mla_mx_step_bf16_kernel(MlaStepArgs a)
             if (KS > 1 && g == 0) tops[set][kg][n] = mx;
         };
         // the probabilities of the wave's keys
-        auto softmax = [&] {
+        auto softmax = [&](int b) {
             int ln = lane;
             asm volatile("" : "+v"(ln));
             const int g = ln >> 4, n = ln & 15;
@@ -215,19 +200,28 @@ __global__ __launch_bounds__(512, 2) void mla_mx_step_bf16_kernel(MlaStepArgs a)
                     lsum += p;
                     pf[r] = (T)p;              // the one rounding of the probabilities, as operands
                 }
-                probs[(NG * kg + h) >> 1][set][ln][(NG * kg + h) & 1] = pf;
+                probs[b][(NG * kg + h) >> 1][set][ln][(NG * kg + h) & 1] = pf;
             }
-            if (g == 0 && kg == 0) factor[set][n] = al;
+            if (g == 0 && kg == 0) factor[b][set][n] = al;
         };
-        // all rows' outputs over the wave's columns
-        auto outputs = [&] {
+        // All rows' outputs over the wave's columns. A transposing read gives a lane
+        // one column of the 16 keys that it holds in both steps of 32, in their order;
+        // the conversions take one scale, so a pair of keys takes two, a half of each.
+        auto outputs = [&](const char* buf, int tb, int pb) {
             int ln = lane;
             asm volatile("" : "+v"(ln));
+            const int g = ln >> 4, key = 16 * (ln >> 2 & 3) + 4 * g + (ln & 3);
+            typedef int32_t i32x2 __attribute__((ext_vector_type(2)));
+            i32x2 codes[ND];
+#pragma unroll
+            for (int d = 0; d < ND; ++d)
+                codes[d] = __builtin_amdgcn_ds_read_tr4_b64_v2i32(
+                    (KDA_LDS i32x2*)(buf + Raw::codes(key, (w * ND + d) >> 1) + 8 * ((w * ND + d) & 1)));
             float f[S];
             bool move = false;
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                f[s] = factor[s][ln & 15];
+                f[s] = factor[pb][s][ln & 15];
                 move |= f[s] != 1.f;
             }
             if (__any(move)) {
@@ -242,48 +236,59 @@ __global__ __launch_bounds__(512, 2) void mla_mx_step_bf16_kernel(MlaStepArgs a)
             for (int u = 0; u < 2; ++u) {                         // 32 keys each
                 Frag<T> p[S];
 #pragma unroll
-                for (int s = 0; s < S; ++s) p[s] = *reinterpret_cast<const Frag<T>*>(&probs[u][s][ln][0]);
+                for (int s = 0; s < S; ++s) p[s] = *reinterpret_cast<const Frag<T>*>(&probs[pb][u][s][ln][0]);
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
-                    const char* const x = wide + u * (32 * DC * 2) + (w * ND + d) * 1024 + ln * 8;
-                    const bf16x4 lo4 = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((KDA_LDS s16x4*)x));
-                    const bf16x4 hi4 = __builtin_bit_cast(bf16x4, __builtin_amdgcn_ds_read_tr16_b64_v4i16((KDA_LDS s16x4*)(x + 512)));
-                    const bf16x8 v = __builtin_shufflevector(lo4, hi4, 0, 1, 2, 3, 4, 5, 6, 7);
+                    uint32_t v[4];
 #pragma unroll
-                    for (int s = 0; s < S; ++s) acc[s][d] = mma16(v, p[s], acc[s][d]);
+                    for (int h = 0; h < 2; ++h) {                 // 16 keys of the tile each
+                        const uint32_t e = *reinterpret_cast<const uint32_t*>(&scales[tb][(w * ND + d) >> 1][32 * u + 16 * h + 4 * g]);
+                        v[2 * h] = h ? mx_pair<2>(codes[d][u], e << 23, e << 15) : mx_pair<0>(codes[d][u], e << 23, e << 15);
+                        v[2 * h + 1] = h ? mx_pair<3>(codes[d][u], e << 7, e >> 1) : mx_pair<1>(codes[d][u], e << 7, e >> 1);
+                    }
+#pragma unroll
+                    for (int s = 0; s < S; ++s) acc[s][d] = mma16(__builtin_bit_cast(bf16x8, u32x4{v[0], v[1], v[2], v[3]}), p[s], acc[s][d]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
         };
         wait_loads_and_lds();
         wg_barrier();
-        int h2 = t0 + 1 < t1 ? fetch(t0 + 1, raw[1]) : 0;
+        int h1 = t0 + 1 < t1 ? fetch(t0 + 1, raw[1]) : 0, h2 = 0;
+        if constexpr (BUFS == 4) h2 = t0 + 2 < t1 ? fetch(t0 + 2, raw[2]) : 0;
         if (scorer) {
             products(raw[0]);
-            maxima(t0, h1);
+            maxima(t0, h0);
         }
-        wait_lds();
-        wg_barrier();
-        if (scorer) softmax();
-        widen(raw[0]);
-        wait_loads_and_lds();
-        wg_barrier();
-        for (int t = t0; t < t1; ++t) {
-            const int i = (t - t0) & 1;
-            const bool more = t + 1 < t1;
-            h1 = h2;
-            if (t + 2 < t1) h2 = fetch(t + 2, raw[i]);
-            if (more && scorer) products(raw[i ^ 1]);
-            outputs();
-            if (more && scorer) maxima(t + 1, h1);
+        turn(raw[0], 0);
+        if constexpr (KS > 1) {
             wait_lds();
             wg_barrier();
+        }
+        if (scorer) softmax(0);
+        if (BUFS == 4 && t0 + 2 < t1) wait_but_last_tile<DC, DR>(w);
+        else wait_loads_and_lds();
+        wg_barrier();
+        for (int t = t0, i = 0; t < t1; ++t) {
+            const int b = (t - t0) & 1, pb = b & (PB - 1), i1 = i == BUFS - 1 ? 0 : i + 1, last = i ? i - 1 : BUFS - 1, have = h1;
+            const bool more = t + 1 < t1, ahead = t + BUFS - 1 < t1;
+            if constexpr (BUFS == 4) h1 = h2;
+            if (ahead) (BUFS == 4 ? h2 : h1) = fetch(t + BUFS - 1, raw[last]);
+            if (more && scorer) products(raw[i1]);
+            outputs(raw[i], b, pb);
             if (more) {
-                if (scorer) softmax();
-                widen(raw[i ^ 1]);
-                wait_loads_and_lds();
+                turn(raw[i1], b ^ 1);
+                if (scorer) maxima(t + 1, have);
+                if constexpr (KS > 1) {
+                    wait_lds();
+                    wg_barrier();
+                }
+                if (scorer) softmax(pb ^ (PB - 1));
+                if (BUFS == 4 && ahead) wait_but_last_tile<DC, DR>(w);
+                else wait_loads_and_lds();
                 wg_barrier();
             }
+            i = i1;
         }
         // every wave needs the rows' sums
         int ln = lane;
@@ -615,7 +620,7 @@ template <class T, int DC, int DR> hipError_t launch_mx(const MlaStepArgs& a, hi
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
     const int blocks = (a.Tq * a.H + a.join_rows - 1) / a.join_rows;
-    mla_step_join_kernel<T, DC, kMaxParts, sizeof(T) == 2 ? kRows : kTile>
+    mla_step_join_kernel<T, DC, sizeof(T) == 2 ? 2 * kMaxParts : kMaxParts, sizeof(T) == 2 ? kRows : kTile>
         <<<dim3((unsigned)((int64_t)a.Nb * blocks)), 256, 0, s>>>(a, blocks);
     return hipGetLastError();
 }
@@ -647,7 +652,7 @@ size_t mla_step_mx_plan(MlaStepArgs& a) {
         a.groups = (int32_t)((blocks + per - 1) / per);
         a.waves = (int32_t)((blocks + a.groups - 1) / a.groups) * 2;
     }
-    int64_t parts = kMaxParts / a.groups;
+    int64_t parts = kMaxParts * (a.bf16 ? residents(a.Dc, a.waves) : 1) / a.groups;
     if (parts < 32) parts = 32;
     if (parts > most) parts = most;
     a.parts = (int32_t)(parts > 1 ? parts : 1);

@@ -35,16 +35,6 @@ template <int DC, int DR> struct RawTile {
     static __device__ __forceinline__ int scales(int r) { return kScalesAt + (r >> 4) * 256 + (r & 15) * NB; }
 };
 
-// Waits for this wave's LDS accesses and its loads, but for those of the last whole
-// tile that it sent on its way (mx_fetch; loads come back in their order).
-template <int DC, int DR> __device__ __forceinline__ void wait_but_last_tile(int w) {
-    constexpr int kLoads = DC / 256 + (DR > 0);
-    asm volatile("" ::: "memory");
-    if (w < 4) __builtin_amdgcn_s_waitcnt(0x0070 | (kLoads + 1));
-    else __builtin_amdgcn_s_waitcnt(0x0070 | kLoads);
-    asm volatile("" ::: "memory");
-}
-
 // Sends the tile of rows k0 .. k0 + 63 of a sequence (of `rows`) on its way to LDS
 // by eight waves (this one w); returns which of its quarters of 16 rows exist. Rows past the
 // sequence and of missing pages are zeros there: their weights are 0, but what

@@ -36,10 +36,11 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
     constexpr int KS = S == 6 ? 1 : S == 4 ? 2 : 4, NG = 4 / KS;
     constexpr int ND = DC / 16 / kWaves, NB = DC / 32, NM = DC / 128, NS = DR / 32;
     constexpr int PB = KS == 1 ? 2 : 1;                          // one barrier a tile, or two
-    constexpr int BUFS = S <= 2 ? 3 : 4;
-    __shared__ __attribute__((aligned(1024))) char raw[BUFS][Raw::kBytes];
+    __shared__ __attribute__((aligned(1024))) char raw[3][Raw::kBytes];
     __shared__ __attribute__((aligned(16))) bf16x4 probs[PB][2][S][64][2];   // of 32 keys each: operands
-    __shared__ __attribute__((aligned(16))) uint8_t scales[2][NB][kRows];    // of a tile, by blocks
+    // a tile's scales by blocks: as numbers; two workgroups' LDS has room for the bytes
+    using Scale = std::conditional_t<(S > 1), uint32_t, uint8_t>;
+    __shared__ __attribute__((aligned(16))) Scale scales[2][NB][kRows];
     __shared__ float factor[PB][S][16], tops[S][KS][16];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool scorer = w < S * KS;
@@ -120,7 +121,7 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
             if (p >= pbase + 64) keep(p, entry(p));
             return mx_fetch<DC, DR>(to, static_cast<const char*>(a.cache), page_bytes, pages, exist, pbase, ps, k0, rows, w, lane);
         };
-        // Tile t lies in raw[(t - t0) % BUFS].
+        // Tile t lies in raw[(t - t0) % 3].
         int h0 = fetch(t0, raw[0]);
         MxQuery16 qm[NM];
         uint32_t qs = 0;                                          // their scale bytes
@@ -138,7 +139,7 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
             if (q < NB / 4) {
                 const uint32_t x = *reinterpret_cast<const uint32_t*>(from + Raw::scales(ln) + 4 * q);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) scales[b][4 * q + i][ln] = (uint8_t)(x >> 8 * i);
+                for (int i = 0; i < 4; ++i) scales[b][4 * q + i][ln] = (Scale)(sizeof(Scale) == 4 ? (x >> 8 * i) << 23 : x >> 8 * i);
             }
         };
         f32x4 acc[S][ND];
@@ -242,9 +243,16 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
                     uint32_t v[4];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {                 // 16 keys of the tile each
-                        const uint32_t e = *reinterpret_cast<const uint32_t*>(&scales[tb][(w * ND + d) >> 1][32 * u + 16 * h + 4 * g]);
-                        v[2 * h] = h ? mx_pair<2>(codes[d][u], e << 23, e << 15) : mx_pair<0>(codes[d][u], e << 23, e << 15);
-                        v[2 * h + 1] = h ? mx_pair<3>(codes[d][u], e << 7, e >> 1) : mx_pair<1>(codes[d][u], e << 7, e >> 1);
+                        const Scale* const at = &scales[tb][(w * ND + d) >> 1][32 * u + 16 * h + 4 * g];
+                        u32x4 e;                                  // exponents; other bits do not count
+                        if constexpr (sizeof(Scale) == 4) {
+                            e = *reinterpret_cast<const u32x4*>(at);
+                        } else {
+                            const uint32_t x = *reinterpret_cast<const uint32_t*>(at);
+                            e = u32x4{x << 23, x << 15, x << 7, x >> 1};
+                        }
+                        v[2 * h] = h ? mx_pair<2>(codes[d][u], e[0], e[1]) : mx_pair<0>(codes[d][u], e[0], e[1]);
+                        v[2 * h + 1] = h ? mx_pair<3>(codes[d][u], e[2], e[3]) : mx_pair<1>(codes[d][u], e[2], e[3]);
                     }
 #pragma unroll
                     for (int s = 0; s < S; ++s) acc[s][d] = mma16(__builtin_bit_cast(bf16x8, u32x4{v[0], v[1], v[2], v[3]}), p[s], acc[s][d]);
@@ -254,8 +262,7 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
         };
         wait_loads_and_lds();
         wg_barrier();
-        int h1 = t0 + 1 < t1 ? fetch(t0 + 1, raw[1]) : 0, h2 = 0;
-        if constexpr (BUFS == 4) h2 = t0 + 2 < t1 ? fetch(t0 + 2, raw[2]) : 0;
+        int h1 = t0 + 1 < t1 ? fetch(t0 + 1, raw[1]) : 0;
         if (scorer) {
             products(raw[0]);
             maxima(t0, h0);
@@ -266,14 +273,12 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
             wg_barrier();
         }
         if (scorer) softmax(0);
-        if (BUFS == 4 && t0 + 2 < t1) wait_but_last_tile<DC, DR>(w);
-        else wait_loads_and_lds();
+        wait_loads_and_lds();
         wg_barrier();
         for (int t = t0, i = 0; t < t1; ++t) {
-            const int b = (t - t0) & 1, pb = b & (PB - 1), i1 = i == BUFS - 1 ? 0 : i + 1, last = i ? i - 1 : BUFS - 1, have = h1;
-            const bool more = t + 1 < t1, ahead = t + BUFS - 1 < t1;
-            if constexpr (BUFS == 4) h1 = h2;
-            if (ahead) (BUFS == 4 ? h2 : h1) = fetch(t + BUFS - 1, raw[last]);
+            const int b = (t - t0) & 1, pb = b & (PB - 1), i1 = i == 2 ? 0 : i + 1, i2 = 3 - i - i1, have = h1;
+            const bool more = t + 1 < t1;
+            if (t + 2 < t1) h1 = fetch(t + 2, raw[i2]);
             if (more && scorer) products(raw[i1]);
             outputs(raw[i], b, pb);
             if (more) {
@@ -284,8 +289,7 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
                     wg_barrier();
                 }
                 if (scorer) softmax(pb ^ (PB - 1));
-                if (BUFS == 4 && ahead) wait_but_last_tile<DC, DR>(w);
-                else wait_loads_and_lds();
+                wait_loads_and_lds();
                 wg_barrier();
             }
             i = i1;

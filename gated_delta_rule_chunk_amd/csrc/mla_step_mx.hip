@@ -262,25 +262,14 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
         };
         wait_loads_and_lds();
         wg_barrier();
-        int h1 = t0 + 1 < t1 ? fetch(t0 + 1, raw[1]) : 0;
-        if (scorer) {
-            products(raw[0]);
-            maxima(t0, h0);
-        }
-        turn(raw[0], 0);
-        if constexpr (KS > 1) {
-            wait_lds();
-            wg_barrier();
-        }
-        if (scorer) softmax(0);
-        wait_loads_and_lds();
-        wg_barrier();
-        for (int t = t0, i = 0; t < t1; ++t) {
-            const int b = (t - t0) & 1, pb = b & (PB - 1), i1 = i == 2 ? 0 : i + 1, i2 = 3 - i - i1, have = h1;
+        // From a tile before the first on, which has no outputs: the first one's scores
+        // are no code of their own (one sequence of 100001: 46 -> 44 us).
+        for (int t = t0 - 1, i = 2; t < t1; ++t) {
+            const int b = (t - t0) & 1, pb = b & (PB - 1), i1 = i == 2 ? 0 : i + 1, i2 = 3 - i - i1, have = h0;
             const bool more = t + 1 < t1;
-            if (t + 2 < t1) h1 = fetch(t + 2, raw[i2]);
+            if (t + 2 < t1) h0 = fetch(t + 2, raw[i2]);
             if (more && scorer) products(raw[i1]);
-            outputs(raw[i], b, pb);
+            if (t >= t0) outputs(raw[i], b, pb);
             if (more) {
                 turn(raw[i1], b ^ 1);
                 if (scorer) maxima(t + 1, have);

@@ -241,6 +241,18 @@ def test_step_large_scores():
     _check_step(ql, qr, rows, o, lse, 5.0, lens)
 
 
+@pytest.mark.parametrize("Dc,Dr", DIMS)
+@pytest.mark.parametrize("H,lens", [(12, [40000, 0, 3]), (24, [33000, 700]), (8, [300] * 130)])
+def test_step_of_few_rows_over_many_parts(Dc, Dr, H, lens):
+    """Two workgroups a compute unit: up to 512 parts, of one sequence or of many."""
+    cache, table, rows = _cache(lens, 64, Dc, Dr, BF16, 24)
+    ql, qr = _queries(len(lens), 1, H, Dc, Dr, BF16, 25)
+    o, lse = kda.mla_step_mx(ql, qr, cache, table, _i32(lens), scale=0.07)
+    _check_step(ql, qr, rows, o, lse, 0.07, lens)
+    again = kda.mla_step_mx(ql, qr, cache, table, _i32(lens), scale=0.07)
+    assert torch.equal(again[0], o) and torch.equal(again[1], lse)
+
+
 @pytest.mark.parametrize("dtype", [BF16, F32])
 def test_step_parts_of_more_pages_than_lanes(dtype):
     """One sequence in 16-row pages, parts of over 64 pages."""
@@ -571,6 +583,68 @@ def test_evict_refuses_sequences_with_missing_pages():
 
 
 # ---- together --------------------------------------------------------------------------------------------------------
+
+
+def test_weigh_many_rows_on_two_streams():
+    """Over 128 rows of queries: calls at once with a workspace each give what they give alone; a short one is refused."""
+    lens, H, T = [700, 33, 0, 400], 20, 9
+    cache, table, rows = _cache(lens, 64, 512, 64, BF16, 52)
+    n, old = _i32(lens), torch.zeros(4, table.shape[1] * 64, device="cuda")
+    need = kda.mla_weigh_workspace_bytes(4, T, H, 512, 64, BF16, 1)
+    calls, want = [], []
+    for k in range(2):
+        ql, qr = _queries(4, T, H, 512, 64, BF16, 53 + k)
+        lse = kda.mla_step_mx(ql, qr, cache, table, n, scale=0.06)[1]
+        calls.append((ql, qr, lse, torch.empty(need, dtype=torch.uint8, device="cuda"), old.clone()))
+        want.append(kda.mla_weigh(ql, qr, cache, table, n, lse, 0.06, old, out=old.clone()))
+        _check_weights(want[k], ql, qr, rows, lse, 0.06, lens, old, T, 1.0, True)
+    torch.cuda.synchronize()
+    streams = [torch.cuda.Stream() for _ in calls]
+    for _ in range(3):
+        for s, (ql, qr, lse, ws, out) in zip(streams, calls):
+            with torch.cuda.stream(s):
+                kda.mla_weigh(ql, qr, cache, table, n, lse, 0.06, old, out=out, workspace=ws)
+    torch.cuda.synchronize()
+    for c, w in zip(calls, want):
+        assert torch.equal(c[4], w)
+    ql, qr, lse, ws, out = calls[0]
+    with pytest.raises(kda.KDAError, match="workspace"):
+        kda.mla_weigh(ql, qr, cache, table, n, lse, 0.06, old, out=out, workspace=ws[:need - 16])
+
+
+@pytest.mark.parametrize("cap", [16384, 40000])
+def test_evict_in_a_graph(cap):
+    """Captured once, replayed with other weights and lengths: one launch that decides, and several."""
+    page, N = 16, 3
+    g = torch.Generator(device="cuda").manual_seed(77)
+    table = torch.randperm(N * cap // page, generator=g, device="cuda").to(torch.int32).view(N, -1)
+    cache = torch.zeros(N * cap // page, page, 136, dtype=torch.uint8, device="cuda")
+    n, w = _i32([cap, 9000, 100]), _weights(g, N, cap)
+    out = torch.empty_like(table), torch.empty_like(n), torch.empty_like(w)
+    ws = torch.empty(kda.mla_evict_workspace_bytes(N, page, cap // page), dtype=torch.uint8, device="cuda")
+
+    def call():
+        kda.mla_evict(cache, table, n, w, 4000, first=5, recent=100, out=out, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for i in range(4):
+        n.copy_(_i32([cap - 1000 * i, 9000 - 1700 * i, 5000 * (i % 2)]))
+        w.copy_(_weights(g, N, cap))
+        for o in out:
+            o.fill_(-5)
+        graph.replay()
+        torch.cuda.synchronize()
+        for b, L in enumerate(n.tolist()):
+            E, a, e, moves, order = ref.evict(w[b, :L].tolist(), L, page, 4000, 5, 100)
+            ww = torch.cat((w[b].cpu()[order], torch.zeros(E * page), w[b, L:].cpu()))
+            assert out[1][b].item() == L - E * page and torch.equal(out[2][b].cpu(), ww)
 
 
 @pytest.mark.parametrize("mx,dtype", [(True, BF16), (False, BF16), (True, F32)])

@@ -38,7 +38,7 @@ struct Work {
     // longer sequences:
     int32_t* hold;                                          // the page table, while it changes in place
     int32_t* bins;                                          // [kPasses][kBins]
-    Counts *counts, *waves;                                 // [parts], [parts][kWaves]
+    Counts *counts, *waves;                                 // [parts]; [parts][kWaves] of the part's waves before
 };
 constexpr int kState = 12;
 __host__ __device__ __forceinline__ int64_t words_a_sequence(int64_t cap, int64_t max_pages) {
@@ -361,15 +361,13 @@ __global__ __launch_bounds__(kThreads) void mla_evict_count_kernel(MlaEvictArgs 
         count(c, k0, (int)j, y.low, last);
         count(c, k1, (int)j + 64, y.low, last);
     }
-    if (lane == 0) {
-        waves[w] = c;
-        y.wk.waves[y.p * kWaves + w] = c;
-    }
+    if (lane == 0) waves[w] = c;
     __syncthreads();
-    if (threadIdx.x == 0) {
-        Counts all{};
-        for (int v = 0; v < kWaves; ++v) add(all, waves[v]);
-        y.wk.counts[y.p] = all;
+    if (threadIdx.x <= kWaves) {                            // of the waves before this one; of all
+        Counts sum{};
+        for (int v = 0; v < kWaves; ++v)
+            if (v < (int)threadIdx.x) add(sum, waves[v]);
+        (threadIdx.x == kWaves ? y.wk.counts[y.p] : y.wk.waves[y.p * kWaves + threadIdx.x]) = sum;
     }
 }
 // The page table: pages from b on close up, the emptied ones come behind them.
@@ -417,7 +415,7 @@ __global__ __launch_bounds__(kThreads) void mla_evict_list_kernel(MlaEvictArgs x
         }
         if (y.p == 0 && threadIdx.x == 0) y.wk.state[2] = movers_of(all, want);
         if (y.j0 < y.j1) {
-            for (int i = 0; i < w; ++i) add(before, y.wk.waves[y.p * kWaves + i]);
+            add(before, y.wk.waves[y.p * kWaves + w]);
             const int64_t run = rows / kWaves, j0 = y.j0 + w * run;
             Listing to{holes_of(before, (int)(j0 < y.low ? j0 : y.low), want), movers_of(before, want),
                        before.low_equal + before.high_equal};

@@ -292,9 +292,10 @@ __device__ __forceinline__ float row_sum(float v) {
 template <int DC, int DR, bool MX, int KS, bool MANY>
 __global__ __launch_bounds__(64 * kWaves, 2) void mla_weigh_bf16_kernel(MlaWeighArgs x, int parts) {
     using Raw = RawTile<DC, DR>;
-    constexpr int RC = (DC + DR) / 8, NG = 4 / KS, kBytes = MX ? Raw::kBytes : kRows * RC * 16;
-    __shared__ __attribute__((aligned(1024))) char tile[2][kBytes];
-    __shared__ __attribute__((aligned(16))) float sums[2][kWaves / KS][kRows];
+    // tiles a turn: queries that pass by meet two, where LDS holds two more
+    constexpr int RC = (DC + DR) / 8, NG = 4 / KS, KT = MANY && MX ? 2 : 1, kBytes = MX ? Raw::kBytes : kRows * RC * 16;
+    __shared__ __attribute__((aligned(1024))) char tile[2][KT][kBytes];
+    __shared__ __attribute__((aligned(16))) float sums[2][kWaves / KS][KT][kRows];
     const MlaStepArgs& a = x.s;
     const int lane = threadIdx.x & 63, w = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int kg = w % KS, slot = w / KS, ps = a.page_shift, sets = (a.Tq * a.H + 15) / 16;
@@ -351,8 +352,13 @@ __global__ __launch_bounds__(64 * kWaves, 2) void mla_weigh_bf16_kernel(MlaWeigh
         };
         const int p0 = t0 * kRows >> ps;
         keep(p0, entry(p0));
-        int have = fetch(t0, tile[0]);
-        Queries<DC, DR, MX> q[MANY ? 2 : 1];
+        int have[KT], next[KT];
+        auto fetch_turn = [&](int t, char (*to)[kBytes], int (&h)[KT]) {
+#pragma unroll
+            for (int j = 0; j < KT; ++j) h[j] = t + j < t1 ? fetch(t + j, to[j]) : 0;
+        };
+        fetch_turn(t0, tile[0], have);
+        Queries<DC, DR, MX> q[MANY && KT == 1 ? 2 : 1];
         auto load = [&](Queries<DC, DR, MX>& y, int set) {
             if (set >= sets) return;
             y.row(x, b, set, lane, len, rows);
@@ -362,59 +368,66 @@ __global__ __launch_bounds__(64 * kWaves, 2) void mla_weigh_bf16_kernel(MlaWeigh
         if constexpr (!MANY) load(q[0], slot);
         wait_loads_and_lds();
         wg_barrier();
-        for (int t = t0; t < t1; ++t) {
-            const int i = (t - t0) & 1, k0 = t * kRows;
-            const char* const buf = tile[i];
-            int next = 0;
-            if (t + 1 < t1) next = fetch(t + 1, tile[i ^ 1]);
-            // the wave that writes the weights reads the old ones now
-            const int key = k0 + lane;
+        for (int t = t0, i = 0; t < t1; t += KT, i ^= 1) {
+            const int k0 = t * kRows;
+            fetch_turn(t + KT, tile[i ^ 1], next);
+            // the waves that write the weights read the old ones now
+            const int mine = kWaves - 1 - w, key = k0 + kRows * mine + lane;
+            const bool writes = mine < KT && t + mine < t1 && key < rows;
             const int64_t at_key = ((int64_t)b * a.max_pages << ps) + key;
             float old = 0.f;
-            if (w == kWaves - 1 && key < rows && x.decay != 0.f && key < len - x.fresh) old = x.decay * x.w_in[at_key];
-            float sum[NG][4];
+            if (writes && x.decay != 0.f && key < len - x.fresh) old = x.decay * x.w_in[at_key];
+            float sum[KT][NG][4];
 #pragma unroll
-            for (int h = 0; h < NG; ++h)
+            for (int j = 0; j < KT; ++j)
 #pragma unroll
-                for (int r = 0; r < 4; ++r) sum[h][r] = 0.f;
-            const bool edge = k0 + kRows > len - a.Tq + 1 || k0 + kRows > rows || have != 15;
+                for (int h = 0; h < NG; ++h)
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) sum[j][h][r] = 0.f;
+            // all rows see all keys of a turn but at its sequence's end
+            const bool edge = k0 + KT * kRows > len - a.Tq + 1 || k0 + KT * kRows > rows || have[0] != 15 || have[KT - 1] != 15;
             auto add = [&](const Queries<DC, DR, MX>& y, bool tail) {
-                f32x4 sc[NG];
                 const int key0 = 16 * NG * kg;
-                if constexpr (MX) {
-                    mx_scores<DC, DR, NG>(buf, key0, lane, y.qm, y.qs, y.qf, sc);
-                } else {
-                    int ln = lane;
-                    asm volatile("" : "+v"(ln));
 #pragma unroll
-                    for (int h = 0; h < NG; ++h) sc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+                for (int j = 0; j < KT; ++j) {
+                    if (j > 0 && t + j >= t1) break;
+                    const char* const buf = tile[i][j];
+                    f32x4 sc[NG];
+                    if constexpr (MX) {
+                        mx_scores<DC, DR, NG>(buf, key0, lane, y.qm, y.qs, y.qf, sc);
+                    } else {
+                        int ln = lane;
+                        asm volatile("" : "+v"(ln));
 #pragma unroll
-                    for (int s = 0; s < (DC + DR) / 32; ++s)
+                        for (int h = 0; h < NG; ++h) sc[h] = f32x4{0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+                        for (int s = 0; s < (DC + DR) / 32; ++s)
+#pragma unroll
+                            for (int h = 0; h < NG; ++h)
+                                sc[h] = mma16(read_rows16<__bf16, RC>(buf, key0 + 16 * h + (ln & 15), s, ln >> 4), y.qf[s], sc[h]);
+#pragma unroll
+                        for (int h = 0; h < NG; ++h) asm volatile("" : "+v"(sc[h]));
+                    }
+                    settle(sc[0], sc[NG - 1]);
+                    if constexpr (NG == 4) settle(sc[1], sc[2]);
+                    if (edge || tail) {
+                        const int lim = y.last - k0 - kRows * j - key0 - 4 * (lane >> 4);
 #pragma unroll
                         for (int h = 0; h < NG; ++h)
-                            sc[h] = mma16(read_rows16<__bf16, RC>(buf, key0 + 16 * h + (ln & 15), s, ln >> 4), y.qf[s], sc[h]);
 #pragma unroll
-                    for (int h = 0; h < NG; ++h) asm volatile("" : "+v"(sc[h]));
-                }
-                settle(sc[0], sc[NG - 1]);
-                if constexpr (NG == 4) settle(sc[1], sc[2]);
-                if (edge || tail) {
-                    const int lim = y.last - k0 - key0 - 4 * (lane >> 4);
+                            for (int r = 0; r < 4; ++r)
+                                sum[j][h][r] += 16 * h + r <= lim && (have[j] >> (NG * kg + h) & 1)
+                                                    ? __builtin_amdgcn_exp2f(__builtin_fmaf(sc[h][r], c, -y.z)) : 0.f;
+                    } else {
 #pragma unroll
-                    for (int h = 0; h < NG; ++h)
+                        for (int h = 0; h < NG; ++h)
 #pragma unroll
-                        for (int r = 0; r < 4; ++r)
-                            sum[h][r] += 16 * h + r <= lim && (have >> (NG * kg + h) & 1)
-                                             ? __builtin_amdgcn_exp2f(__builtin_fmaf(sc[h][r], c, -y.z)) : 0.f;
-                } else {
-#pragma unroll
-                    for (int h = 0; h < NG; ++h)
-#pragma unroll
-                        for (int r = 0; r < 4; ++r) sum[h][r] += __builtin_amdgcn_exp2f(__builtin_fmaf(sc[h][r], c, -y.z));
+                            for (int r = 0; r < 4; ++r) sum[j][h][r] += __builtin_amdgcn_exp2f(__builtin_fmaf(sc[h][r], c, -y.z));
+                    }
                 }
             };
-            if constexpr (MANY) {
-                // the rows behind the last are in the last set
+            // (the rows behind the last are in the last set)
+            if constexpr (MANY && KT == 1) {
                 load(q[0], w);
                 for (int s = w; s < sets; s += 2 * kWaves) {
                     load(q[1], s + kWaves);
@@ -424,27 +437,36 @@ __global__ __launch_bounds__(64 * kWaves, 2) void mla_weigh_bf16_kernel(MlaWeigh
                         add(q[1], s + kWaves == sets - 1);
                     }
                 }
+            } else if constexpr (MANY) {
+                for (int s = w; s < sets; s += kWaves) {
+                    load(q[0], s);
+                    add(q[0], s == sets - 1);
+                }
             } else if (slot < sets) {
                 add(q[0], slot == sets - 1);
             }
             if (MANY || slot < sets) {
 #pragma unroll
-                for (int h = 0; h < NG; ++h) {
-                    f32x4 v;
+                for (int j = 0; j < KT; ++j)
 #pragma unroll
-                    for (int r = 0; r < 4; ++r) v[r] = row_sum(sum[h][r]);
-                    if ((lane & 15) == 0) *reinterpret_cast<f32x4*>(&sums[i][slot][16 * (NG * kg + h) + 4 * (lane >> 4)]) = v;
-                }
+                    for (int h = 0; h < NG; ++h) {
+                        f32x4 v;
+#pragma unroll
+                        for (int r = 0; r < 4; ++r) v[r] = row_sum(sum[j][h][r]);
+                        if ((lane & 15) == 0)
+                            *reinterpret_cast<f32x4*>(&sums[i][slot][j][16 * (NG * kg + h) + 4 * (lane >> 4)]) = v;
+                    }
             }
             wait_loads_and_lds();
             wg_barrier();
-            if (w == kWaves - 1 && key < rows) {
+            if (writes) {
                 const int n = MANY ? kWaves : sets;
                 float v = 0.f;
-                for (int s = 0; s < n; ++s) v += sums[i][s][lane];
+                for (int s = 0; s < n; ++s) v += sums[i][s][mine][lane];
                 x.w_out[at_key] = old + v;
             }
-            have = next;
+#pragma unroll
+            for (int j = 0; j < KT; ++j) have[j] = next[j];
         }
         wait_lds();
         wg_barrier();                                             // the next sequence's first tile overwrites a buffer
@@ -469,7 +491,7 @@ template <int DC, int DR, bool MX> hipError_t launch_weigh_bf16(const MlaWeighAr
     const int sets = (a.Tq * a.H + 15) / 16;
     const int64_t cap = (int64_t)a.max_pages << a.page_shift, units = a.Nb * ((cap + kRows - 1) / kRows);
     // queries stay: a part a compute unit; of many sets they do not, and smaller parts even out
-    const int64_t most = sets <= kSets ? 256 : 1024;
+    const int64_t most = sets <= kSets || MX ? 256 : 1024;
     const int parts = (int)(units < most ? units : most);
     const dim3 grid((unsigned)parts);
     if (sets <= 2) mla_weigh_bf16_kernel<DC, DR, MX, 4, false><<<grid, 64 * kWaves, 0, s>>>(x, parts);

@@ -37,10 +37,11 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
     constexpr int ND = DC / 16 / kWaves, NB = DC / 32, NM = DC / 128, NS = DR / 32;
     constexpr int PB = KS == 1 ? 2 : 1;                          // one barrier a tile, or two
     __shared__ __attribute__((aligned(1024))) char raw[3][Raw::kBytes];
-    __shared__ __attribute__((aligned(16))) bf16x4 probs[PB][2][S][64][2];   // of 32 keys each: operands
-    // a tile's scales by blocks: as numbers; two workgroups' LDS has room for the bytes
-    using Scale = std::conditional_t<(S > 1), uint32_t, uint8_t>;
-    __shared__ __attribute__((aligned(16))) Scale scales[2][NB][kRows];
+    __shared__ __attribute__((aligned(16))) s16x4 probs[PB][2][S][64][2];   // of 32 keys each: operands
+    // A tile's scales by blocks: as numbers, or (one set) as the exponents of bf16.
+    using Scale = std::conditional_t<(S > 1), uint32_t, uint16_t>;
+    constexpr int kExponent = S > 1 ? 23 : 7;
+    __shared__ __attribute__((aligned(16))) Scale scales[PB][NB][kRows];
     __shared__ float factor[PB][S][16], tops[S][KS][16];
     const int tid = threadIdx.x, lane = tid & 63, w = __builtin_amdgcn_readfirstlane(tid >> 6);
     const bool scorer = w < S * KS;
@@ -139,7 +140,7 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
             if (q < NB / 4) {
                 const uint32_t x = *reinterpret_cast<const uint32_t*>(from + Raw::scales(ln) + 4 * q);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) scales[b][4 * q + i][ln] = (Scale)(sizeof(Scale) == 4 ? (x >> 8 * i) << 23 : x >> 8 * i);
+                for (int i = 0; i < 4; ++i) scales[b][4 * q + i][ln] = (Scale)((x >> 8 * i & 255) << kExponent);
             }
         };
         f32x4 acc[S][ND];
@@ -186,7 +187,7 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
             }
             // the running maximum moves as in mla_step.hip
             float al = 1.f;
-            if ((mx - m) * c > 8.f) {
+            if ((mx - m) * c > (S > 1 ? 8.f : 0.f)) {
                 al = __builtin_amdgcn_exp2f((m - mx) * c);
                 lsum *= al;
                 m = mx;
@@ -194,21 +195,33 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
             const float m0 = m == -INFINITY ? 0.f : m;            // nothing seen yet: all terms are 0
 #pragma unroll
             for (int h = 0; h < NG; ++h) {
+                float p[4];
                 bf16x4 pf;
 #pragma unroll
                 for (int r = 0; r < 4; ++r) {
-                    const float p = __builtin_amdgcn_exp2f((sc[h][r] - m0) * c);
-                    lsum += p;
-                    pf[r] = (T)p;              // the one rounding of the probabilities, as operands
+                    p[r] = __builtin_amdgcn_exp2f((sc[h][r] - m0) * c);
+                    lsum += p[r];
+                    pf[r] = (T)p[r];           // the one rounding of the probabilities, as operands
                 }
-                probs[b][(NG * kg + h) >> 1][set][ln][(NG * kg + h) & 1] = pf;
+                s16x4 bits = __builtin_bit_cast(s16x4, pf);
+                if constexpr (S == 1) {
+#pragma unroll
+                    for (int r = 0; r < 4; ++r) bits[r] = p[r] < 0x1p-126f ? -32768 : bits[r] - (127 << 7);
+                }
+                probs[b][(NG * kg + h) >> 1][set][ln][(NG * kg + h) & 1] = bits;
             }
             if (g == 0 && kg == 0) factor[b][set][n] = al;
         };
         // All rows' outputs over the wave's columns. A transposing read gives a lane
-        // one column of the 16 keys that it holds in both steps of 32, in their order;
-        // the conversions take one scale, so a pair of keys takes two, a half of each.
-        auto outputs = [&](const char* buf, int tb, int pb) {
+        // one column of the 16 keys that it holds in both steps of 32, in their order.
+        // The conversions take one scale, where the two codes of a byte are of two
+        // keys: a pair takes two conversions, a half of each. For one set it costs
+        // less to scale the probabilities, which then are at most 1 (a maximum moves
+        // at once): as bf16's bits, 127 << 7 less, a scale's exponent is added, and
+        // what is negative then is 0, as are those of zeros, -32768, at any scale.
+        // (A block of NaN needs none: it made its row's sum NaN.) 64 sequences of
+        // 16384, 12 heads: 92 us with scaled pairs, 83 with scaled probabilities.
+        auto outputs = [&](const char* buf, int b) {
             int ln = lane;
             asm volatile("" : "+v"(ln));
             const int g = ln >> 4, key = 16 * (ln >> 2 & 3) + 4 * g + (ln & 3);
@@ -222,7 +235,7 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
             bool move = false;
 #pragma unroll
             for (int s = 0; s < S; ++s) {
-                f[s] = factor[pb][s][ln & 15];
+                f[s] = factor[b][s][ln & 15];
                 move |= f[s] != 1.f;
             }
             if (__any(move)) {
@@ -235,27 +248,34 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
             }
 #pragma unroll
             for (int u = 0; u < 2; ++u) {                         // 32 keys each
-                Frag<T> p[S];
+                typedef int16_t s16x8 __attribute__((ext_vector_type(8)));
+                s16x8 p[S];
 #pragma unroll
-                for (int s = 0; s < S; ++s) p[s] = *reinterpret_cast<const Frag<T>*>(&probs[pb][u][s][ln][0]);
+                for (int s = 0; s < S; ++s) p[s] = *reinterpret_cast<const s16x8*>(&probs[b][u][s][ln][0]);
+                if constexpr (S == 1) {
+#pragma unroll
+                    for (int d = 0; d < ND; ++d) {
+                        const Scale* const at = &scales[b][(w * ND + d) >> 1][32 * u + 4 * g];
+                        const s16x4 e0 = *reinterpret_cast<const s16x4*>(at), e1 = *reinterpret_cast<const s16x4*>(at + 16);
+                        const s16x8 y = p[0] + __builtin_shufflevector(e0, e1, 0, 1, 2, 3, 4, 5, 6, 7);
+                        acc[0][d] = mma16(MxScale(127).bf16(codes[d][u]),
+                                          __builtin_bit_cast(bf16x8, __builtin_elementwise_max(y, (s16x8)0)), acc[0][d]);
+                    }
+                    __builtin_amdgcn_sched_barrier(0);
+                    continue;
+                }
 #pragma unroll
                 for (int d = 0; d < ND; ++d) {
                     uint32_t v[4];
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {                 // 16 keys of the tile each
-                        const Scale* const at = &scales[tb][(w * ND + d) >> 1][32 * u + 16 * h + 4 * g];
-                        u32x4 e;                                  // exponents; other bits do not count
-                        if constexpr (sizeof(Scale) == 4) {
-                            e = *reinterpret_cast<const u32x4*>(at);
-                        } else {
-                            const uint32_t x = *reinterpret_cast<const uint32_t*>(at);
-                            e = u32x4{x << 23, x << 15, x << 7, x >> 1};
-                        }
+                        const Scale* const at = &scales[b][(w * ND + d) >> 1][32 * u + 16 * h + 4 * g];
+                        const u32x4 e = *reinterpret_cast<const u32x4*>(at);
                         v[2 * h] = h ? mx_pair<2>(codes[d][u], e[0], e[1]) : mx_pair<0>(codes[d][u], e[0], e[1]);
                         v[2 * h + 1] = h ? mx_pair<3>(codes[d][u], e[2], e[3]) : mx_pair<1>(codes[d][u], e[2], e[3]);
                     }
 #pragma unroll
-                    for (int s = 0; s < S; ++s) acc[s][d] = mma16(__builtin_bit_cast(bf16x8, u32x4{v[0], v[1], v[2], v[3]}), p[s], acc[s][d]);
+                    for (int s = 0; s < S; ++s) acc[s][d] = mma16(__builtin_bit_cast(bf16x8, u32x4{v[0], v[1], v[2], v[3]}), __builtin_bit_cast(bf16x8, p[s]), acc[s][d]);
                 }
                 __builtin_amdgcn_sched_barrier(0);
             }
@@ -265,19 +285,22 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
         // From a tile before the first on, which has no outputs: the first one's scores
         // are no code of their own (one sequence of 100001: 46 -> 44 us).
         for (int t = t0 - 1, i = 2; t < t1; ++t) {
-            const int b = (t - t0) & 1, pb = b & (PB - 1), i1 = i == 2 ? 0 : i + 1, i2 = 3 - i - i1, have = h0;
+            const int b = (t - t0) & (PB - 1), i1 = i == 2 ? 0 : i + 1, i2 = 3 - i - i1, have = h0;
             const bool more = t + 1 < t1;
             if (t + 2 < t1) h0 = fetch(t + 2, raw[i2]);
-            if (more && scorer) products(raw[i1]);
-            if (t >= t0) outputs(raw[i], b, pb);
+            if (more && scorer) {
+                products(raw[i1]);
+                if (t < t0) settle(sc[0], sc[NG - 1]);            // (no outputs follow)
+            }
+            if (t >= t0) outputs(raw[i], b);
             if (more) {
-                turn(raw[i1], b ^ 1);
                 if (scorer) maxima(t + 1, have);
                 if constexpr (KS > 1) {
                     wait_lds();
                     wg_barrier();
                 }
-                if (scorer) softmax(pb ^ (PB - 1));
+                turn(raw[i1], b ^ (PB - 1));
+                if (scorer) softmax(b ^ (PB - 1));
                 wait_loads_and_lds();
                 wg_barrier();
             }

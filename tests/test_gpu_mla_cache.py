@@ -241,6 +241,32 @@ def test_step_large_scores():
     _check_step(ql, qr, rows, o, lse, 5.0, lens)
 
 
+@pytest.mark.parametrize("H", [8, 24, 96])
+@pytest.mark.parametrize("std", [0.7, 40.0])
+def test_step_latents_of_all_magnitudes(H, std):
+    """Blocks from 2^-97 to 2^100, keys of one block up to 2^40 apart, weights spread and on a few keys."""
+    lens, Dc, page = [200, 33, 1], 256, 16
+    g = torch.Generator(device="cuda").manual_seed(26)
+    table, total = _table(lens, page, g, 1)
+    cache = torch.zeros((total, page, kda.mla_mx_row_bytes(Dc, 0, BF16)), dtype=torch.uint8, device="cuda")
+    powers = torch.tensor([-97.0, -60.0, 0.0, 0.0, 0.0, 20.0, 60.0, 98.0], device="cuda").repeat_interleave(32)
+    rows = []
+    for i, n in enumerate(lens):
+        spread = torch.zeros(n, 8, device="cuda")
+        spread[:, 4] = torch.randint(-20, 21, (n,), generator=g, device="cuda").float()
+        x = _rand(g, F32, n, Dc).double() * ref.power((powers + spread.repeat_interleave(32, 1)).long())
+        c, s = ref.encode(x.float())
+        rows.append((ref.values(c, s), None))
+        for k in range(0, n, page):
+            ref.put_page(cache, table[i, k // page].item(), c[k:k + page], s[k:k + page], None)
+    ql, _ = _queries(len(lens), 1, H, Dc, 0, BF16, 27)
+    ql = (ql / 0.7 * std).to(BF16)
+    ql[..., :64] = 0                                             # scores by the two blocks of 2^0
+    ql[..., 128:] = 0
+    o, lse = kda.mla_step_mx(ql, None, cache, table.cuda(), _i32(lens), scale=0.06)
+    _check_step(ql, None, rows, o, lse, 0.06, lens)
+
+
 @pytest.mark.parametrize("Dc,Dr", DIMS)
 @pytest.mark.parametrize("H,lens", [(12, [40000, 0, 3]), (24, [33000, 700]), (8, [300] * 130)])
 def test_step_of_few_rows_over_many_parts(Dc, Dr, H, lens):

@@ -110,10 +110,6 @@ template <int S> __device__ __forceinline__ f32x4 mma_mx16(const u32x4& a, const
     const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};     // (4-bit operands take four registers)
     return __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(x, b, c, 4, 0, S, (int)sa, S, (int)sb);
 }
-template <int S> __device__ __forceinline__ f32x16 mma_mx32(const u32x4& a, const i32x8& b, f32x16 c, uint32_t sa, uint32_t sb) {
-    const i32x8 x = {(int)a[0], (int)a[1], (int)a[2], (int)a[3], 0, 0, 0, 0};
-    return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, b, c, 4, 0, S, (int)sa, S, (int)sb);
-}
 
 // The scale byte of a block whose largest magnitude has these float32 bits: e + 127
 // for the least e with it <= 7 * 2^e, at most 125.

@@ -2,15 +2,9 @@
 // (include/kda_mla_cache.h): s = scale (q_latent . c + q_rope . r), p = softmax s,
 // o = sum p c.
 //
-// As in mla_step.hip the tiles of 32 cache rows of all sequences form one list,
-// cut into equal parts by the lengths on the device, and a second kernel joins
-// the parts. A tile's codes come to registers a tile ahead, 32 channels a
-// thread, and are written to LDS as T. Four waves share a block of 32 rows of
-// queries: each forms the scores of 16 rows and 16 keys, the two that share
-// rows agree on the running maximum, and each multiplies the probabilities of
-// all 32 rows with a quarter of the columns. So neither queries, scores nor outputs
-// (Dc / 8 registers) take more than a third of a SIMD's registers, and three
-// blocks (96 rows) leave each SIMD three waves.
+// As in mla_step.hip the tiles of cache rows of all sequences (64 rows, float32
+// 32) form one list, cut into equal parts by the lengths on the device, and a
+// second kernel joins the parts.
 #include "mla_mx_tile.hpp"
 #include "mla_step.hpp"
 
@@ -19,15 +13,22 @@ namespace {
 
 // float32: blocks of 32 rows of queries a workgroup, at most (as queries and outputs fit the registers)
 __host__ __device__ constexpr int most_blocks(int dc) { return dc == 256 ? 2 : 1; }
-// bf16: workgroups a compute unit, as registers and LDS allow
+// bf16: workgroups a compute unit, as registers and LDS allow; a part for each
 __host__ __device__ constexpr int residents(int dc, int sets) { return sets == 1 || (sets == 2 && dc == 256) ? 2 : 1; }
-// bf16. Eight waves share up to six sets of 16 rows of queries and tiles of 64 keys.
-// For the scores a set has one wave, or two or four that take 16-key groups of the
-// tile each (and tell each other their maxima); every wave multiplies all rows'
-// probabilities with an eighth of the columns, so that each value operand is read
-// from LDS once. A tile's scores are formed along with the outputs of the one
-// before; the softmax and the widening of the latents to bf16 come between; the
-// loads of the next tile, straight into LDS, are under way all the while.
+// bf16. Eight waves share up to six sets of 16 rows of queries and tiles of 64 keys,
+// which come straight to LDS as they lie in memory, two ahead of the outputs.
+// Scores run on the codes (mla_mx_tile.hpp). A set has one wave for them, or two or
+// four that take 16-key groups of the tile each and tell each other their maxima;
+// every wave multiplies all rows' probabilities with an eighth of the columns, whose
+// codes it turns and widens to bf16 in registers, each once a tile. A tile's
+// scores are formed before the outputs of the one before.
+// Bound, with six sets, by matrix (36%) and vector instructions (43% of the cycles),
+// which two waves a SIMD seldom overlap: 3.2 us a tile, 128 sequences of 4096 to
+// 8192, 96 heads in 205-220 us, 760 TFLOP/s. Measured and not kept, same case: a
+// widened copy of the tile in LDS for the outputs (217), four tile buffers (227),
+// half of the waves a phase behind the others (213). With one set, by vector
+// instructions (66%): 64 sequences of 8192 to 16384, 12 heads in 83 us, 2.5 TB/s;
+// two workgroups a compute unit (one: 100 us).
 template <int DC, int DR, int S>
 __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_kernel(MlaStepArgs a) {
     using T = __bf16;
@@ -285,22 +286,22 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
         // From a tile before the first on, which has no outputs: the first one's scores
         // are no code of their own (one sequence of 100001: 46 -> 44 us).
         for (int t = t0 - 1, i = 2; t < t1; ++t) {
-            const int b = (t - t0) & (PB - 1), i1 = i == 2 ? 0 : i + 1, i2 = 3 - i - i1, have = h0;
+            const int now = (t - t0) & (PB - 1), i1 = i == 2 ? 0 : i + 1, i2 = 3 - i - i1, have = h0;
             const bool more = t + 1 < t1;
             if (t + 2 < t1) h0 = fetch(t + 2, raw[i2]);
             if (more && scorer) {
                 products(raw[i1]);
                 if (t < t0) settle(sc[0], sc[NG - 1]);            // (no outputs follow)
             }
-            if (t >= t0) outputs(raw[i], b);
+            if (t >= t0) outputs(raw[i], now);
             if (more) {
                 if (scorer) maxima(t + 1, have);
                 if constexpr (KS > 1) {
                     wait_lds();
                     wg_barrier();
                 }
-                turn(raw[i1], b ^ (PB - 1));
-                if (scorer) softmax(b ^ (PB - 1));
+                turn(raw[i1], now ^ (PB - 1));
+                if (scorer) softmax(now ^ (PB - 1));
                 wait_loads_and_lds();
                 wg_barrier();
             }
@@ -356,7 +357,13 @@ __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_ke
 }
 
 // float32: a tile's codes come to registers a tile ahead, 32 channels a thread,
-// and go to LDS as float32 rows, which scores and outputs read.
+// and go to LDS as float32 rows, which scores and outputs read. Four waves share a
+// block of 32 rows of queries: each forms the scores of 16 rows and 16 keys, the two
+// that share rows agree on the running maximum, and each multiplies the
+// probabilities of all 32 rows with a quarter of the columns. Two blocks for Dc =
+// 256; one for 512, where queries and outputs take the registers of two. 8
+// sequences of 1024 to 2047, 3 new tokens, 16 heads, Dc = 256 in 25 us, bound by the
+// latency of two tiles in a row.
 template <int DC, int DR, int RB> __global__ __launch_bounds__(256 * RB, RB) void mla_mx_step_f32_kernel(MlaStepArgs a) {
     using T = float;
     constexpr int D = DC + DR, RC = D / kChunk<T>, NS = D / 32, ND = DC / 64, NT = 256 * RB;

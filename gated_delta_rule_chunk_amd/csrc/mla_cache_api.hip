@@ -141,6 +141,9 @@ kda_status kda_mla_weigh(const void* q_latent, int64_t q_latent_n, int64_t q_lat
         r.apart("workspace", workspace, "cache", cache);
         r.apart("workspace", workspace, "weights_out", weights_out);
         r.apart("workspace", workspace, "q_latent", q_latent);
+        r.apart("workspace", workspace, "q_rope", q_rope);
+        r.apart("workspace", workspace, "lse", lse);
+        r.apart("workspace", workspace, "weights", weights);
         if (r.st != KDA_OK) return r.st;
     }
     x.split = static_cast<char*>(workspace);

@@ -153,6 +153,7 @@ def test_step_refuses(lib, kw, status, needle):
     (dict(out=P[5]), BAD, "alias lse"), (dict(out=P[0]), BAD, "alias q_latent"),
     (dict(H=129), BAD, "workspace"), (dict(H=129, ws=P[8], n=1000), BAD, "workspace"), (dict(H=129, ws=ODD, n=1 << 30), BAD, "workspace"),
     (dict(H=129, ws=P[7], n=1 << 30), BAD, "workspace must not alias weights_out"),
+    (dict(H=129, ws=P[5], n=1 << 30), BAD, "workspace must not alias lse"),
 ])
 def test_weigh_refuses(lib, kw, status, needle):
     assert _weigh(lib, **kw) == status

@@ -104,6 +104,7 @@ __global__ __launch_bounds__(256, sizeof(T) == 2 ? 2 : 1) void mla_fwd_kernel(Ml
                 }
             }
         if constexpr (sizeof(T) == 2) sched_reads_under_mma<larger(DQ / 32, 2), 1, DQ / 16 * KB - larger(DQ / 32, 2)>();
+        settle(sc[0], sc[KB - 1]);                       // the branches below can be taken right behind the products
         // hide keys past the sequence or after the row
         if (k0 + BN > Lk || (a.causal && k0 + BN - 1 > wq0 + off)) {
             int lim = Lk - 1 - k0;

@@ -42,9 +42,11 @@ typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
 
 // bf16 queries as the sum of two e4m3 numbers each, hi 2^(s - 127) + lo 2^(s - 131),
 // with an s for each block of 32 channels: s puts the largest into [128, 256), hi
-// rounds to 4 significant bits, and what is left of bf16's 8 fits 4 more. Exact for
-// channels down to 2^-14 of the largest; smaller ones lose at most 2^-21 of it,
-// where lo's smallest steps end. A block with a NaN or an infinity gets s = 255, NaN.
+// rounds to 4 significant bits, and what is left of bf16's 8 fits 4 more, down to
+// 2^-6: channels from 2^-13 of the largest on. Smaller ones lose at most half of
+// lo's smallest step, 2^-14 2^(s - 127), 2^-21 of the largest; s is no less than 9,
+// so where the largest is below 2^-111 any may lose 2^-132. A block with a NaN or
+// an infinity gets s = 255, NaN.
 __device__ __forceinline__ uint32_t query_max(const bf16x8& a, const bf16x8& b) {     // largest magnitude, as bits
     uint32_t m = 0;
 #pragma unroll

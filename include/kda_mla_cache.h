@@ -70,9 +70,10 @@ kda_status kda_mla_cache_read_mx(const void* cache, const int32_t* page_table, c
  * kda_mla_step over the 4-bit cache. Arguments, rules and errors as there.
  * The scores of KDA_BF16 run on the scaled matrix instructions with the 4-bit
  * codes as they stand; a query of bf16 is two 8-bit floats (e4m3) there, whose
- * sum is the query itself except for channels below 2^-14 of the largest of
- * their 32, which are off by at most 2^-21 of that. KDA_F32 runs on the float32
- * matrix cores. A NaN block reaches the sequences that hold it and no others.
+ * sum is the query itself except for channels below 2^-13 of the largest of
+ * their 32, which are off by at most 2^-21 of that; where the largest is below
+ * 2^-111, any of them by at most 2^-132. KDA_F32 runs on the float32 matrix
+ * cores. A NaN block reaches the sequences that hold it and no others.
  */
 size_t kda_mla_step_mx_workspace_bytes(int32_t Nb, int32_t Tq, int32_t H, int32_t Dc, int32_t page_size,
                                        int32_t max_pages, kda_dtype dtype);
@@ -90,7 +91,8 @@ kda_status kda_mla_step_mx(const void* q_latent, int64_t q_latent_n, int64_t q_l
  * tokens, rows that attention has no use for stay low.)
  *
  *   q_latent, q_rope, cache, page_table, seq_lens, sizes, scale, dtype
- *              as in kda_mla_step; form 0: cache as in kda_mla.h, 1: 4-bit
+ *              as in kda_mla_step; form 0: cache as in kda_mla.h, 1: 4-bit, whose
+ *              scores are those of kda_mla_step_mx
  *   lse        [Nb,Tq,H] float32
  *   weights, weights_out  [Nb, max_pages * page_size] float32, the same memory
  *              (in place) or apart. Rows from seq_lens[n] on are neither read nor

@@ -1,0 +1,59 @@
+"""The 4-bit cache of latents and what works on it, further: the precision of split queries."""
+import math
+
+import pytest
+import torch
+
+import gated_delta_rule_chunk_amd as kda
+from tests import mla_cache_ref as ref
+from tests import mla_ref
+from tests.test_gpu_mla_cache import BF16, _i32
+from tests.test_mla_split_host import stated
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.mark.parametrize("H,call", [(128, "step"), (16, "step"), (128, "weigh"), (256, "weigh")])
+def test_split_queries(H, call):
+    """One key, 2^K in the channel of x: the score is x 2^K, with nothing to add to it. x has every significand, from
+    2^-7 of the block's largest down, for largest ones at either end of their exponent."""
+    exact, loss, tiny, least = stated()
+    tops = [-133, -126, -120, -112, -111, -60, 0, 100]
+    cases = [(t, big, d) for t in tops for big in (1.0, 1.9921875) for d in range(7, 25) if t >= -126 or big == 1.0]
+    Nb, Dc, page = len(cases), 256, 16
+    j = torch.arange(H, device="cuda")
+    ql = torch.zeros(Nb, 1, H, Dc, dtype=BF16, device="cuda")
+    codes = torch.zeros(Nb, Dc, dtype=torch.uint8)
+    scales = torch.full((Nb, Dc // 32), 127, dtype=torch.uint8)
+    want, bound = [], []
+    for b, (t, big, d) in enumerate(cases):
+        block, at = b % 8, 32 * (b % 8) + (5 * b) % 32
+        L = (torch.tensor(big) * 2.0 ** t).to(BF16).item()
+        sign = 1 - 2 * (j % 2).double()
+        x = (sign * (1 + (j * max(1, 128 // H) % 128) / 128) * 2.0 ** max(t - d, -200)).to(BF16)
+        ql[b, 0, :, 32 * block + (5 * b + 7 + b % 3) % 32] = L
+        ql[b, 0, :, at] = x
+        K = max(-100, min(125, d - t))
+        codes[b, at] = 2
+        scales[b, at // 32] = 127 + K
+        v = x.double()
+        off = torch.full_like(v, least) if L < tiny else torch.where(v.abs() >= exact * L, 0.0, loss * L)
+        want.append(v * 2.0 ** K)
+        bound.append(off * 2.0 ** K)
+    want, bound = torch.stack(want), torch.stack(bound)
+    cache = kda.mla_cache_mx(Nb, page, Dc, 0, BF16)
+    for b in range(Nb):
+        ref.put_page(cache, b, codes[b:b + 1].cuda(), scales[b:b + 1].cuda(), None)
+    table, n = _i32([[b] for b in range(Nb)]), _i32([1] * Nb)
+    if call == "step":
+        # lse is the score in base 2 and back: three roundings, and of the scale
+        o, lse = kda.mla_step_mx(ql, None, cache, table, n, 1.0)
+        assert bool(((lse[:, 0].double() - want).abs() <= bound + 6 * mla_ref.H32 * want.abs() + 2.0 ** -140).all())
+    else:
+        # exp(x 2^K - 0), summed over the heads: one head's share is seen by giving the others an lse of infinity
+        for h in range(0, H, 37):
+            lse = torch.full((Nb, 1, H), math.inf, device="cuda")
+            lse[:, 0, h] = 0
+            w = kda.mla_weigh(ql, None, cache, table, n, lse, 1.0, torch.zeros(Nb, page, device="cuda"))[:, 0].double()
+            off = bound[:, h] + 8 * mla_ref.H32 * (1 + want[:, h].abs())
+            assert bool(((w - want[:, h].exp()).abs() <= want[:, h].exp() * torch.expm1(off)).all()), h

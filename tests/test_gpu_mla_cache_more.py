@@ -1,4 +1,5 @@
-"""The 4-bit cache of latents and what works on it, further: the precision of split queries."""
+"""The 4-bit cache of latents and what works on it, further: the precision of split queries, weights over missing
+pages."""
 import math
 
 import pytest
@@ -7,7 +8,7 @@ import torch
 import gated_delta_rule_chunk_amd as kda
 from tests import mla_cache_ref as ref
 from tests import mla_ref
-from tests.test_gpu_mla_cache import BF16, _i32
+from tests.test_gpu_mla_cache import BF16, F32, _cache, _i32, _limits, _queries, _rows_of_queries
 from tests.test_mla_split_host import stated
 
 pytestmark = pytest.mark.gpu
@@ -57,3 +58,53 @@ def test_split_queries(H, call):
             w = kda.mla_weigh(ql, None, cache, table, n, lse, 1.0, torch.zeros(Nb, page, device="cuda"))[:, 0].double()
             off = bound[:, h] + 8 * mla_ref.H32 * (1 + want[:, h].abs())
             assert bool(((w - want[:, h].exp()).abs() <= want[:, h].exp() * torch.expm1(off)).all()), h
+
+
+# page size, lengths, missing pages by sequence: in the first and in the second tile of a pair, whole tiles, quarters,
+# one behind another, the last page, the first; past the 64 pages of a window
+HOLES = [
+    (16, [1100, 300, 64, 45], [[1, 4, 5, 6, 7, 20, 66], [0, 18], [3], [2]]),
+    (32, [700, 190, 33], [[1, 2, 3, 21], [0, 4], [1]]),
+    (64, [520, 64, 129], [[0, 3, 4], [0], [2]]),
+    (128, [600, 250], [[1, 3], [0]]),
+]
+
+
+@pytest.mark.parametrize("mx", [True, False])
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("H,T", [(8, 1), (48, 1), (100, 1), (130, 1), (50, 3), (5, 4)])
+@pytest.mark.parametrize("page,lens,holes", HOLES)
+def test_weights_and_attention_over_missing_pages(mx, dtype, H, T, page, lens, holes):
+    """Every number of rows of queries that has a kernel of its own: what exists gets its weight, what does not keeps
+    the old one, decayed; each missing page is counted once."""
+    scale = 0.07
+    cache, table, rows = _cache(lens, page, 512, 64, dtype, H + T, mx=mx)
+    ql, qr = _queries(len(lens), T, H, 512, 64, dtype, 9)
+    bad = table.clone()
+    for b, gone in enumerate(holes):
+        for i, p in enumerate(gone):
+            bad[b, p] = -1 if i % 2 else cache.shape[0] + i
+    count = f"{sum(len(x) for x in holes)} counted"
+    n = _i32(lens)
+    o, lse = (kda.mla_step_mx if mx else kda.mla_step)(ql, qr, cache, bad, n, scale=scale)
+    with pytest.raises(kda.KDAError, match=count):
+        kda.device_check()
+    g = torch.Generator(device="cuda").manual_seed(10)
+    old = torch.rand((len(lens), table.shape[1] * page), generator=g, device="cuda")
+    out = torch.full_like(old, 7.0)
+    kda.mla_weigh(ql, qr, cache, bad, n, lse, scale, old, fresh=0, decay=0.5, out=out)
+    with pytest.raises(kda.KDAError, match=count):
+        kda.device_check()
+    for b, L in enumerate(lens):
+        j = torch.arange(L, device="cuda")
+        there = ~torch.isin(j // page, torch.tensor(holes[b], device="cuda"))
+        at = j[there]
+        c, r = rows[b][0][at], rows[b][1][at]
+        limit = (at[None] < _limits(L, T, H, L)[:, None]).sum(1)
+        q = _rows_of_queries(ql, qr, b)
+        res = ref.attend(q, c, r, scale, limit, dtype, mx)
+        mla_ref.check(f"o[{b}]", o[b].reshape(1, T * H, 512), res["o"])
+        mla_ref.check(f"lse[{b}]", lse[b].reshape(1, T * H), res["lse"])
+        w = ref.gathered(q, c, r, lse[b].flatten(), scale, limit, old[b, at], 0.5, dtype, mx)
+        mla_ref.check(f"weights[{b}]", out[b, at], w)
+        assert torch.equal(out[b, :L][~there], 0.5 * old[b, :L][~there]) and bool((out[b, L:] == 7).all())

@@ -1,5 +1,5 @@
 """The 4-bit cache of latents and what works on it, further: the precision of split queries, weights over missing
-pages."""
+pages, and page offsets past 2^32 bytes for the weights of either form and for eviction."""
 import math
 
 import pytest
@@ -8,7 +8,8 @@ import torch
 import gated_delta_rule_chunk_amd as kda
 from tests import mla_cache_ref as ref
 from tests import mla_ref
-from tests.test_gpu_mla_cache import BF16, F32, _cache, _i32, _limits, _queries, _rows_of_queries
+from tests.test_gpu_mla_cache import (BF16, F32, _cache, _evict_and_check, _i32, _limits, _queries, _rows_of_queries,
+                                      _weights)
 from tests.test_mla_split_host import stated
 
 pytestmark = pytest.mark.gpu
@@ -108,3 +109,24 @@ def test_weights_and_attention_over_missing_pages(mx, dtype, H, T, page, lens, h
         w = ref.gathered(q, c, r, lse[b].flatten(), scale, limit, old[b, at], 0.5, dtype, mx)
         mla_ref.check(f"weights[{b}]", out[b, at], w)
         assert torch.equal(out[b, :L][~there], 0.5 * old[b, :L][~there]) and bool((out[b, L:] == 7).all())
+
+
+@pytest.mark.parametrize("mx,dtype,n_pages", [(True, BF16, 43000), (True, F32, 32500), (False, BF16, 14700), (False, F32, 7400)])
+def test_weights_and_eviction_past_four_gib(mx, dtype, n_pages):
+    """All pages that are used lie past 2^32 bytes: what is moved, from there to there, and what is weighed."""
+    page, lens = 256, [1400, 45, 900]
+    cache, table, rows = _cache(lens, page, 512, 64, dtype, 6, mx=mx, n_pages=n_pages)
+    used = table[table >= 0]
+    assert int(used.min()) * page * cache.shape[2] * cache.element_size() > 1 << 32
+    for H in (8, 130):
+        ql, qr = _queries(3, 1, H, 512, 64, dtype, 7)
+        lse = (kda.mla_step_mx if mx else kda.mla_step)(ql, qr, cache, table, _i32(lens), 0.07)[1]
+        w = torch.zeros(3, table.shape[1] * page, device="cuda")
+        kda.mla_weigh(ql, qr, cache, table, _i32(lens), lse, 0.07, w)
+        for b, (c, r) in enumerate(rows):
+            q, L = _rows_of_queries(ql, qr, b), lens[b]
+            mla_ref.check(f"weights[{b}]", w[b, :L], ref.gathered(q, c, r, lse[b].flatten(), 0.07, _limits(L, 1, H, L),
+                                                                  torch.zeros(L, device="cuda"), 1.0, dtype, mx))
+    # (NaN rows are behind the lengths and in pages that nobody has: compared as bytes)
+    g = torch.Generator(device="cuda").manual_seed(8)
+    _evict_and_check(cache, table, _i32(lens), _weights(g, 3, table.shape[1] * page), 300, 3, 100, True)

@@ -1,5 +1,6 @@
 """The 4-bit cache of latents and what works on it, further: the precision of split queries, weights over missing
-pages, and page offsets past 2^32 bytes for the weights of either form and for eviction."""
+pages, page offsets past 2^32 bytes for the weights of either form and for eviction, and what eviction moves when it is
+replayed."""
 import math
 
 import pytest
@@ -130,3 +131,65 @@ def test_weights_and_eviction_past_four_gib(mx, dtype, n_pages):
     # (NaN rows are behind the lengths and in pages that nobody has: compared as bytes)
     g = torch.Generator(device="cuda").manual_seed(8)
     _evict_and_check(cache, table, _i32(lens), _weights(g, 3, table.shape[1] * page), 300, 3, 100, True)
+
+
+@pytest.mark.parametrize("form", ["mx", "rows"])
+@pytest.mark.parametrize("cap", [16384, 40000])
+def test_what_eviction_moves_when_replayed(cap, form):
+    """Captured once, replayed with other weights, lengths and page tables: rows, page table, lengths and weights, by
+    one launch that decides and by several."""
+    page, N, keep, first, recent = 16, 3, 4000, 5, 100
+    g = torch.Generator(device="cuda").manual_seed(78)
+    pages = N * cap // page
+    if form == "mx":
+        make = lambda: torch.randint(0, 256, (pages, page, 136), dtype=torch.uint8, device="cuda", generator=g)  # noqa: E731
+    else:
+        make = lambda: torch.randn((pages, page, 256), device="cuda", generator=g).to(BF16)  # noqa: E731
+    shuffled = lambda: torch.randperm(pages, generator=g, device="cuda").to(torch.int32).view(N, -1)  # noqa: E731
+    cache, table, n, w = make(), shuffled(), _i32([cap, 9000, 100]), _weights(g, N, cap)
+    out = torch.empty_like(table), torch.empty_like(n), torch.empty_like(w)
+    ws = torch.empty(kda.mla_evict_workspace_bytes(N, page, cap // page), dtype=torch.uint8, device="cuda")
+
+    def call():
+        kda.mla_evict(cache, table, n, w, keep, first=first, recent=recent, out=out, workspace=ws)
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call()
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    parts = ((0, 128), (128, 8)) if form == "mx" else ((0, 512),)       # a row's bytes in a page of 16
+
+    def bytes_of(x):                                                     # by rows
+        x = x.view(torch.uint8).view(pages, -1)
+        return torch.cat([x[:, at * page:(at + k) * page].reshape(pages * page, k) for at, k in parts], 1)
+
+    moved = 0
+    for i in range(4):
+        cache.copy_(make())
+        table.copy_(shuffled())
+        n.copy_(_i32([cap - 1000 * i, 9000 - 1700 * i, 5000 * (i % 2)]))
+        w.copy_(_weights(g, N, cap))
+        for x in out:
+            x.fill_(-5)
+        want, t0 = bytes_of(cache).clone(), table.tolist()
+        before = want.clone()
+        graph.replay()
+        if i % 2:
+            torch.cuda.synchronize()
+        for b, L in enumerate(n.tolist()):
+            E, a, e, moves, order = ref.evict(w[b, :L].tolist(), L, page, keep, first, recent)
+            t, used = t0[b], -(-L // page)
+            assert out[0][b].tolist() == (t[:e - E] + t[e:used] + t[e - E:e] + t[used:] if E else t)
+            ww = torch.cat((w[b].cpu()[order], torch.zeros(E * page), w[b, L:].cpu()))
+            assert out[1][b].item() == L - E * page and torch.equal(out[2][b].cpu(), ww)
+            if moves:
+                to, src = (torch.tensor([t[j // page] * page + j % page for j in x], device="cuda") for x in zip(*moves))
+                want[to] = before[src]
+                moved += len(moves)
+        assert torch.equal(bytes_of(cache), want)
+        assert table.tolist() == t0
+    assert moved > 10000

@@ -1,6 +1,6 @@
 """The 4-bit cache of latents and what works on it, further: the precision of split queries, weights over missing
 pages, page offsets past 2^32 bytes for the weights of either form and for eviction, and what eviction moves when it is
-replayed."""
+replayed; outputs in place and apart, calls replayed from a graph, shared queries."""
 import math
 
 import pytest
@@ -193,3 +193,88 @@ def test_what_eviction_moves_when_replayed(cap, form):
         assert torch.equal(bytes_of(cache), want)
         assert table.tolist() == t0
     assert moved > 10000
+
+
+@pytest.mark.parametrize("apart", [(1, 0, 0), (0, 1, 0), (0, 0, 1), (0, 1, 1), (1, 0, 1), (1, 1, 0)])
+@pytest.mark.parametrize("cap", [16384, 40000])
+def test_evict_some_in_place_some_apart(cap, apart):
+    """Page table, lengths and weights, each in place or apart, give what all in place give."""
+    page, lens = 16, [12000, 700, -3, 4097, cap]
+    g = torch.Generator(device="cuda").manual_seed(79)
+    pages = len(lens) * cap // page
+    cache = torch.randint(0, 256, (pages, page, 136), dtype=torch.uint8, device="cuda", generator=g)
+    table = torch.randperm(pages, generator=g, device="cuda").to(torch.int32).view(len(lens), -1)
+    state = table, _i32(lens), _weights(g, len(lens), cap)
+    first, mine = cache.clone(), [x.clone() for x in state]
+    want = kda.mla_evict(first, *mine, 3000, first=20, recent=500)
+    out = tuple(torch.full_like(x, -9) if a else x for x, a in zip(state, apart))
+    kept = [x.clone() for x in state]
+    got = kda.mla_evict(cache, *state, 3000, first=20, recent=500, out=out)
+    assert torch.equal(cache, first)
+    for x, y, o, s, k, a in zip(got, want, out, state, kept, apart):
+        assert x is o and torch.equal(x, y)
+        assert not a or torch.equal(s, k)
+
+
+@pytest.mark.parametrize("mx,dtype,Dc,H,T", [(True, BF16, 512, 12, 1), (True, BF16, 512, 40, 4), (False, BF16, 256, 40, 4),
+                                             (False, BF16, 512, 100, 1), (True, F32, 256, 12, 1), (False, F32, 512, 40, 2)])
+def test_write_read_attention_and_weights_replayed(mx, dtype, Dc, H, T):
+    """Captured once, replayed with other lengths, queries and new rows: what the same calls give eagerly."""
+    page, N, room = 16, 3, 30
+    g = torch.Generator(device="cuda").manual_seed(95)
+    rand = lambda *s: torch.randn(s, generator=g, device="cuda").to(dtype)  # noqa: E731
+    table = torch.randperm(N * room, generator=g, device="cuda").to(torch.int32).view(N, room)
+    cache = kda.mla_cache_mx(N * room, page, Dc, 64, dtype) if mx else torch.zeros((N * room, page, Dc + 64), dtype=dtype, device="cuda")
+    append, step = (kda.mla_cache_append_mx, kda.mla_step_mx) if mx else (kda.mla_cache_append, kda.mla_step)
+    append(rand(N, 400, Dc), rand(N, 400, 64), cache, table, _i32([0] * N))
+    s = {"cache": cache, "n": _i32([0] * N), "c": rand(N, T, Dc), "r": rand(N, T, 64), "ql": rand(N, T, H, Dc),
+         "qr": rand(N, T, H, 64), "w": torch.zeros(N, room * page, device="cuda")}
+    cu = _i32([0, 30, 30, 75])
+
+    def call(s):
+        append(s["c"], s["r"], s["cache"], table, s["n"])
+        s["n"].add_(T)
+        o, lse = step(s["ql"], s["qr"], s["cache"], table, s["n"], 0.07)
+        w = kda.mla_weigh(s["ql"], s["qr"], s["cache"], table, s["n"], lse, 0.07, s["w"], decay=0.9)
+        return (o, lse, w) + (kda.mla_cache_read_mx(s["cache"], table, cu, 80, Dc, dtype, starts=s["n"]) if mx else ())
+
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        call(s)
+    torch.cuda.current_stream().wait_stream(side)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = call(s)
+    for i, lens in enumerate(([100, 7, 300], [0, 64, 399], [33, -9, 200], [1, 2, 63])):
+        for k in ("c", "r", "ql", "qr"):
+            s[k].copy_(rand(*s[k].shape))
+        s["n"].copy_(_i32(lens))
+        s["w"].copy_(_weights(g, *s["w"].shape))
+        twin = {k: v.clone() for k, v in s.items()}
+        graph.replay()
+        if i % 2:
+            torch.cuda.synchronize()
+        want = call(twin)
+        for x, y in zip(out, want):
+            assert torch.equal(x, y), lens
+        assert torch.equal(s["cache"], twin["cache"])
+
+
+@pytest.mark.parametrize("dtype", [BF16, F32])
+@pytest.mark.parametrize("mx", [True, False])
+def test_queries_that_heads_or_tokens_share(mx, dtype):
+    """Strides of zero: one query for all heads, and one for all tokens."""
+    lens, T, H = [70, 5, 200], 3, 44
+    cache, table, _ = _cache(lens, 32, 512, 64, dtype, 96, mx=mx)
+    n, old = _i32(lens), torch.zeros(3, table.shape[1] * 32, device="cuda")
+    step = kda.mla_step_mx if mx else kda.mla_step
+    for shape in ((3, T, 1), (3, 1, H), (1, T, H)):
+        g = torch.Generator(device="cuda").manual_seed(97)
+        q = [torch.randn((*shape, D), generator=g, device="cuda").to(dtype).expand(3, T, H, D) for D in (512, 64)]
+        o, lse = step(*q, cache, table, n, 0.07)
+        w = kda.mla_weigh(*q, cache, table, n, lse, 0.07, old, out=old.clone())
+        q = [x.contiguous() for x in q]
+        want = step(*q, cache, table, n, 0.07)
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+        assert torch.equal(w, kda.mla_weigh(*q, cache, table, n, lse, 0.07, old, out=old.clone()))

@@ -9,12 +9,12 @@
  * a latent share a scale 2^e; each is held as a 4-bit code of a multiple of it:
  * codes 0 to 7 stand for 0, 0.5, 1, 1.5, 2, 3, 4, 6, bit 3 is the sign. The
  * scale is a byte e + 127. e is the smallest with max|c| <= 7 * 2^e, at most 125,
- * so that no rounding is off by more than 2^e; values are rounded to the nearest
- * multiple, ties to the even code, past 6 to 6. A block whose largest magnitude
- * is below 2^-100 is held as zeros (codes and scale byte 0); a block with a NaN
- * or an infinity as NaN (scale byte 255). The key part r that the heads share
- * keeps its dtype: its scores are the sensitive ones, and it is a ninth of a
- * row's channels.
+ * so that no rounding is off by more than 2^e, or in blocks of more than 7 * 2^125
+ * by 2 * 2^e; values are rounded to the nearest multiple, ties to the even code,
+ * past 6 to 6. A block whose largest magnitude is below 2^-100 is held as zeros
+ * (codes and scale byte 0); a block with a NaN or an infinity as NaN (scale byte
+ * 255). The key part r that the heads share keeps its dtype: its scores are the
+ * sensitive ones, and it is a ninth of a row's channels.
  * A page of page_size rows is, in this order,
  *     page_size * Dc / 2   bytes of codes (channel 2 i in the low half of byte i)
  *     page_size * Dc / 32  scale bytes

@@ -72,7 +72,9 @@ kda_status kda_mla_cache_read_mx(const void* cache, const int32_t* page_table, c
  * codes as they stand; a query of bf16 is two 8-bit floats (e4m3) there, whose
  * sum is the query itself except for channels below 2^-13 of the largest of
  * their 32, which are off by at most 2^-21 of that; where the largest is below
- * 2^-111, any of them by at most 2^-132. KDA_F32 runs on the float32 matrix
+ * 2^-111, any of them by at most 2^-132. Of the outputs, the product of a
+ * weight (before the division by their sum) and a block's 2^e below 2^-126 may
+ * count as 0: 6 * 2^-126 a row at most. KDA_F32 runs on the float32 matrix
  * cores. A NaN block reaches the sequences that hold it and no others.
  */
 size_t kda_mla_step_mx_workspace_bytes(int32_t Nb, int32_t Tq, int32_t H, int32_t Dc, int32_t page_size,

@@ -2,6 +2,7 @@
 pages, page offsets past 2^32 bytes for the weights of either form and for eviction, and what eviction moves when it is
 replayed; outputs in place and apart, calls replayed from a graph, shared queries."""
 import math
+import re
 
 import pytest
 import torch
@@ -11,7 +12,7 @@ from tests import mla_cache_ref as ref
 from tests import mla_ref
 from tests.test_gpu_mla_cache import (BF16, F32, _cache, _evict_and_check, _i32, _limits, _queries, _rows_of_queries,
                                       _weights)
-from tests.test_mla_split_host import stated
+from tests.test_mla_split_host import HEADER, stated
 
 pytestmark = pytest.mark.gpu
 
@@ -278,3 +279,38 @@ def test_queries_that_heads_or_tokens_share(mx, dtype):
         want = step(*q, cache, table, n, 0.07)
         assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
         assert torch.equal(w, kda.mla_weigh(*q, cache, table, n, lse, 0.07, old, out=old.clone()))
+
+
+@pytest.mark.parametrize("H,pages", [(8, 4), (16, 4096), (32, 4096), (64, 4096), (96, 4096)])
+def test_weights_times_scales_next_to_nothing(H, pages):
+    """A block that only rows of small weight have, of values that float32 can just hold: weight times scale passes
+    2^-126 on the way. Each row's part is off by no more than the header says, whatever the number of sets."""
+    Dc, page = 256, 64
+    codes = torch.zeros(2 + 40, Dc, dtype=torch.uint8)
+    scales = torch.full((42, Dc // 32), 127, dtype=torch.uint8)
+    codes[:2, 0] = 2                                             # two rows of a score of 0, with zeros in block 5
+    for k in range(40):                                          # the others: scores below 0, values 1 to 6 2^e
+        codes[2 + k, 160:192] = torch.arange(32) % 6 + 2
+        scales[2 + k, 5] = 25 + k % 3
+        codes[2 + k, 32] = 4
+        codes[2 + k, 64:67] = torch.tensor([2, 2, 2]) if k % 2 else torch.tensor([0, 0, 0])
+    values = ref.values(codes, scales).cuda()
+    cache = kda.mla_cache_mx(1, page, Dc, 0, BF16)
+    ref.put_page(cache, 0, codes.cuda(), scales.cuda(), None)
+    table = torch.full((1, pages), -1, dtype=torch.int32, device="cuda")
+    table[0, 0] = 0
+    ql = torch.zeros(1, 1, H, Dc, dtype=BF16, device="cuda")
+    ql[..., 32] = -(torch.arange(H, device="cuda") % 12).to(BF16)        # weights down to e^-23
+    ql[..., 64:67] = -0.5
+    o, lse = kda.mla_step_mx(ql, None, cache, table, _i32([42]), 1.0)
+    q = ql[0, 0].double()
+    p = torch.softmax(q @ values.t(), -1)
+    want = p @ values
+    m = re.search(r"may count as 0: (\d) \* 2\^-(\d+) a row at most", re.sub(r"\n \* *", " ", open(HEADER).read()))
+    least = int(m.group(1)) * 2.0 ** -int(m.group(2))
+    for h in range(H):
+        # weights and result rounded to bf16, scores of up to 24 as the float32 they are
+        got = o[0, 0, h].double()
+        off = (2.0 ** -7 + 2.0 ** -13) * (p[h] @ values.abs()) + 42 * least
+        assert bool(((got - want[h]).abs() <= off).all()), h
+    assert bool((want[:, 160:] > 0).any())

@@ -5,7 +5,7 @@
 
 namespace {
 
-// rows of a sequence, all sequences counted, that weights are indexed by
+// the cache's form: 0 rows of dtype, 1 latents in 4 bits
 kda_status check_form(const char* fn, int32_t form) {
     if (form != 0 && form != 1) return fail(KDA_ERR_INVALID_ARG, "%s: form must be 0 or 1, got %d", fn, form);
     return KDA_OK;
@@ -56,7 +56,7 @@ kda_status kda_mla_cache_read_mx(const void* cache, const int32_t* page_table, c
     if (kda_status st = check_cache(fn, cache, page_table, cu_seqlens, n_pages, page_size, max_pages, Dc, Dr, dtype,
                                     a.page_shift))
         return st;
-    if ((int64_t)T > kMaxGrid * 256 / (Dc / 8 + 16))             // a thread for each 8 channels of a row
+    if ((int64_t)T > kMaxGrid * 256 / (Dc / 8 + 16))             // as the header has it; the grid would hold more, 16 rows a workgroup
         return fail(KDA_ERR_UNSUPPORTED, "%s: problem too large: T = %d", fn, T);
     if (!latent || (Dr == 0) != (k_rope == nullptr))
         return fail(KDA_ERR_INVALID_ARG, "%s: latent must be non-NULL, k_rope NULL if and only if Dr = 0", fn);

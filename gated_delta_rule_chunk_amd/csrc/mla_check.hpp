@@ -88,7 +88,7 @@ kda_status check_append(const char* fn, const void* latent, int64_t latent_row, 
     if (kda_status st = check_cache(fn, cache, page_table, cache_lens, n_pages, page_size, max_pages, Dc, Dr, dtype,
                                     a.page_shift))
         return st;
-    // a thread for each 16 bytes of a token
+    // a thread for each 16 bytes of a token (the 4-bit write has the same limit, though its grid would hold more)
     if ((int64_t)B * T > kMaxGrid * 256 / ((Dc + Dr) * (dtype == KDA_BF16 ? 2 : 4) / 16))
         return fail(KDA_ERR_UNSUPPORTED, "%s: problem too large: B * T = %lld", fn, (long long)B * T);
     if (!latent || (Dr == 0) != (k_rope == nullptr))

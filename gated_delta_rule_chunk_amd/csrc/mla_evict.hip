@@ -39,7 +39,7 @@ struct Counts {
     int low, low_equal, high, high_equal;                   // rows above and at the last key that stays, by side
 };
 struct Work {
-    int32_t* state;                                         // length, pages that go, moves, -; the key and how many equal ones stay: [4..9]
+    int32_t* state;                                         // length, pages that go, moves, -; the key so far and how many rows of it stay, by passes: [4..11]
     int32_t *dst, *src;                                     // rows by their places in the new page table
     float* val;                                             // the weights that move
     // longer sequences:

@@ -78,8 +78,6 @@ __device__ __forceinline__ void query_split(const bf16x8& q, int at, uint32_t s,
     lo = l;
 }
 
-typedef int32_t i32x8 __attribute__((ext_vector_type(8)));
-
 // Operands of a step of 128 products on 16x16 tiles, codes against e4m3: lane l
 // with g = l / 16 holds of the codes the 32 products from 32 g, but of the 8-bit
 // numbers the 16 from 16 g and the 16 from 64 + 16 g (measured); its scale bytes are those

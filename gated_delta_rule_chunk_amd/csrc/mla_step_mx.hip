@@ -546,7 +546,7 @@ template <int DC, int DR, int RB> __global__ __launch_bounds__(256 * RB, RB) voi
             for (int r = 0; r < 4; ++r) {
                 const float p = __builtin_amdgcn_exp2f((sc[r] - m0) * c);
                 lsum += p;
-                pf[r] = (T)p;                  // bf16: the one rounding of the probabilities, as operands
+                pf[r] = p;
             }
 #pragma unroll
             for (int r = 0; r < 4; ++r) probs[rb][rh][ln][4 * kh + r] = pf[r];

@@ -59,7 +59,8 @@ kda_status kda_mla_cache_append_mx(const void* latent, int64_t latent_row, int64
  *               two is a bf16 number)
  *   zero_rest   as in kda_mla.h, for rows behind the last sequence
  * Rows past the page table, before row 0 or in pages that do not exist are
- * written as zeros and reported by kda_device_check. T = 0 is a no-op.
+ * written as zeros and reported by kda_device_check. T = 0 is a no-op;
+ * T * (Dc / 8 + 16) past 2^32 - 256 is refused.
  */
 kda_status kda_mla_cache_read_mx(const void* cache, const int32_t* page_table, const int32_t* starts,
                                  const int32_t* cu_seqlens, int32_t n_pages, int32_t page_size, int32_t max_pages,

@@ -28,7 +28,9 @@ __host__ __device__ constexpr int residents(int dc, int sets) { return sets == 1
 // widened copy of the tile in LDS for the outputs (217), four tile buffers (227),
 // half of the waves a phase behind the others (213). With one set, by vector
 // instructions (66%): 64 sequences of 8192 to 16384, 12 heads in 83 us, 2.5 TB/s;
-// two workgroups a compute unit (one: 100 us).
+// two workgroups a compute unit (one: 100 us). The matrix cores take bf16, so the
+// probabilities are rounded once, as operands, their sum is not: o is off by
+// 0.0017-0.0018 of its norm, where its own rounding alone leaves 0.0017.
 template <int DC, int DR, int S>
 __global__ __launch_bounds__(512, 2 * residents(DC, S)) void mla_mx_step_bf16_kernel(MlaStepArgs a) {
     using T = __bf16;

@@ -21,6 +21,9 @@
  *     page_size * Dr       elements of dtype
  * each of them row by row: kda_mla_mx_row_bytes(Dc, Dr, dtype) bytes a row (400
  * for Dc = 512, Dr = 64, KDA_BF16, where a row of kda_mla.h's cache has 1152).
+ * What it gives is room: with many heads, where products bound the attention, a
+ * step over one sequence takes as long as over kda_mla.h's cache or a little
+ * longer; batches, and few heads, gain time too.
  * The cache is 16-byte aligned. Dc in {256, 512}, Dr in {0, 64}, page_size a
  * power of two from 16 to 2^24, max_pages * page_size at most 2^30.
  */
